@@ -39,6 +39,12 @@ SIGNATURES = {
     "kda_backward": (_i, [_vp] * 5 + [_f] + [_vp] * 9 + [_i] * 7 + [_vp, _sz, _vp]),
     "kda_backward_ex_workspace_size": (_sz, [_i] * 7),
     "kda_backward_ex": (_i, [_vp] * 5 + [_f] + [_vp] * 9 + [_i] * 8 + [_vp, _sz, _vp]),
+    "kda_scan_workspace_size": (_sz, [_i] * 5),
+    "kda_scan_checkpoint_size": (_sz, [_i] * 3),
+    "kda_scan_fwd": (_i, [_vp] * 4 + [_i] + [_vp] * 3 + [_i] * 6 + [_vp, _sz, _vp]),
+    "kda_scan_backward": (_i, [_vp] * 7 + [_i] + [_vp] * 3 + [_i] * 6 + [_vp, _sz, _vp]),
+    "kda_scan_backward_ckpt": (_i, [_vp] * 4 + [_i] + [_vp] * 3 + [_i] * 6 + [_vp, _sz, _vp]),
+    "kda_scan_step": (_i, [_vp] * 5 + [_i] * 5 + [_vp]),
 }
 
 # kda_gate: how the forget gate enters the update (see include/kda.h)
@@ -46,6 +52,8 @@ KDA_GATE_CHANNEL, KDA_GATE_HEAD, KDA_GATE_NONE = 0, 1, 2
 # kda_prep bits: raw inputs prepared inside the kernels (see include/kda.h)
 KDA_PREP_L2NORM_QK, KDA_PREP_GATE_LOGSIGMOID, KDA_PREP_BETA_SIGMOID = 1, 2, 4
 KDA_PREP_ALL = KDA_PREP_L2NORM_QK | KDA_PREP_GATE_LOGSIGMOID | KDA_PREP_BETA_SIGMOID
+# kda_scan_input: the weight of the input in the elementwise recurrence (1, or 1 - alpha)
+KDA_SCAN_INPUT_PLAIN, KDA_SCAN_INPUT_COMPLEMENT = 0, 1
 
 
 def _gate_kind(g, lead):
@@ -341,3 +349,178 @@ def kda_backward(q, k, v, g, beta, grad_o, scale=None, initial_state=None, grad_
     if st != KDA_OK:
         raise KDAError(st, "kda_backward")
     return out
+
+
+def kda_scan_workspace_size(B, T, D, num_seqs=0, dtype=torch.bfloat16) -> int:
+    return int(load().kda_scan_workspace_size(B, T, D, num_seqs, _dtype_code(dtype)))
+
+
+def kda_scan_checkpoint_size(B, T, D) -> int:
+    """Bytes of the 8-bit activation checkpoint of kda_scan_fwd (its layout: include/kda.h)."""
+    return int(load().kda_scan_checkpoint_size(B, T, D))
+
+
+def _scan_check(device, shape, dtype, cu_seqlens, tensors, states):
+    """Checks what the scan calls share; returns (B, T, D, number of packed sequences).
+    ``tensors``: name -> [B, T, D] tensor, ``states``: name -> fp32 state, either may be None."""
+    if len(shape) != 3:
+        raise ValueError("the sequence tensors must be [B,T,D]")
+    for name, x in tensors.items():
+        if x is not None:
+            _check_dev(name, x, dtype)
+            if x.shape != shape or x.device != device:
+                raise ValueError(f"{name} must be {list(shape)} on {device}")
+    B, T, D = shape
+    seqs = 0
+    if cu_seqlens is not None:
+        _check_dev("cu_seqlens", cu_seqlens, torch.int32)
+        if cu_seqlens.dim() != 1 or cu_seqlens.numel() < 2 or cu_seqlens.device != device:
+            raise ValueError(f"cu_seqlens must be [num_seqs + 1], num_seqs >= 1, on {device}")
+        if B != 1:
+            raise ValueError("packed sequences (cu_seqlens) need B = 1")
+        seqs = cu_seqlens.numel() - 1
+    for name, x in states.items():
+        if x is not None:
+            _check_dev(name, x, torch.float32)
+            if x.shape != (seqs or B, D) or x.device != device:
+                raise ValueError(f"{name} must be [{seqs or B}, {D}] on {device}")
+    return B, T, D, seqs
+
+
+def _scan_run(name, device, stream, args, shape, code, prep, input_gate, seqs, workspace, made):
+    """Calls a scan entry point with its workspace.  ``made``: the tensors allocated here, which a
+    stream other than the current one must be recorded with."""
+    lib = load()
+    B, T, D = shape
+    need = lib.kda_scan_workspace_size(B, T, D, seqs, code)
+    if workspace is None and need:
+        workspace = torch.empty(need, dtype=torch.uint8, device=device)
+        made.append(workspace)
+    elif workspace is not None:
+        _check_dev("workspace", workspace)
+    nbytes = 0 if workspace is None else workspace.numel() * workspace.element_size()
+    with _on(device):
+        st = getattr(lib, name)(*args, B, T, D, code, int(prep), int(input_gate), _ptr(workspace), nbytes,
+                                _stream(stream, device))
+    _record(made, stream, device)
+    if st != KDA_OK:
+        raise KDAError(st, name)
+
+
+def _record(made, stream, device):
+    if stream is not None and stream != torch.cuda.current_stream(device):
+        for t in made:
+            t.record_stream(stream)
+
+
+def kda_scan_fwd(x, g, initial_state=None, *, cu_seqlens=None, input_gate=KDA_SCAN_INPUT_PLAIN, prep=0, h=None,
+                 final_state=None, output_final_state=True, checkpoint=None, workspace=None, stream=None):
+    """Elementwise gated linear recurrence h_t = alpha_t h_{t-1} + w_t x_t over x, g [B,T,D] (fp32 or bf16, CUDA).
+
+    alpha = exp(g), or sigmoid(g) with ``prep=KDA_PREP_GATE_LOGSIGMOID``; w = 1
+    (KDA_SCAN_INPUT_PLAIN) or 1 - alpha (KDA_SCAN_INPUT_COMPLEMENT).  States are [B,D] fp32.
+    ``cu_seqlens``: int32 [num_seqs + 1] on the device, packed sequences along the T rows of B = 1
+    (states [num_seqs,D]); rows outside every sequence get zeros.
+    ``checkpoint``: a uint8 tensor of kda_scan_checkpoint_size(B, T, D) bytes to fill with the 8-bit
+    activation checkpoint that kda_scan_backward_ckpt reads.
+    Returns (h [B,T,D] in the input dtype, final_state or None); ``final_state`` may be
+    ``initial_state`` itself.
+    """
+    _check_dev("x", x)
+    code = _dtype_code(x.dtype)
+    B, T, D, seqs = _scan_check(x.device, x.shape, x.dtype, cu_seqlens, {"g": g, "h": h},
+                                {"initial_state": initial_state, "final_state": final_state})
+    if checkpoint is not None:
+        _check_ckpt(checkpoint, x.shape, x.device)
+    made = []
+    if h is None:
+        h = torch.empty_like(x)
+        made.append(h)
+    if final_state is None and output_final_state:
+        final_state = torch.empty((seqs or B, D), dtype=torch.float32, device=x.device)
+        made.append(final_state)
+    args = (_ptr(x), _ptr(g), _ptr(initial_state), _ptr(cu_seqlens), seqs, _ptr(h), _ptr(final_state),
+            _ptr(checkpoint))
+    _scan_run("kda_scan_fwd", x.device, stream, args, (B, T, D), code, prep, input_gate, seqs, workspace, made)
+    return h, final_state
+
+
+def _check_ckpt(checkpoint, shape, device):
+    _check_dev("checkpoint", checkpoint, torch.uint8)
+    need = kda_scan_checkpoint_size(*shape)
+    if checkpoint.device != device or checkpoint.numel() < need:
+        raise ValueError(f"checkpoint must hold {need} bytes on {device}")
+
+
+def _scan_grads(like, seqs, want_initial_state_grad, made):
+    out = dict(dx=torch.empty_like(like), dg=torch.empty_like(like), dS0=None)
+    if want_initial_state_grad:
+        out["dS0"] = torch.empty((seqs or like.shape[0], like.shape[2]), dtype=torch.float32, device=like.device)
+    made.extend(t for t in out.values() if t is not None)
+    return out
+
+
+def kda_scan_backward(x, g, h, grad_h, initial_state=None, grad_final_state=None, *, cu_seqlens=None,
+                      input_gate=KDA_SCAN_INPUT_PLAIN, prep=0, workspace=None, stream=None,
+                      want_initial_state_grad=True):
+    """Gradients of a loss through kda_scan_fwd (same ``prep``, ``input_gate``, ``cu_seqlens``), given its inputs,
+    its output h, grad_h = dL/dh and grad_final_state = dL/d final_state (or None).  x may be None for
+    KDA_SCAN_INPUT_PLAIN.  Returns a dict: dx, dg (input dtype) and dS0 fp32 (None if not wanted).
+    """
+    _check_dev("grad_h", grad_h)
+    code = _dtype_code(grad_h.dtype)
+    if input_gate == KDA_SCAN_INPUT_COMPLEMENT and x is None:
+        raise ValueError("x is needed for KDA_SCAN_INPUT_COMPLEMENT")
+    B, T, D, seqs = _scan_check(grad_h.device, grad_h.shape, grad_h.dtype, cu_seqlens, {"x": x, "g": g, "h": h},
+                                {"initial_state": initial_state, "grad_final_state": grad_final_state})
+    made = []
+    out = _scan_grads(grad_h, seqs, want_initial_state_grad, made)
+    args = (_ptr(x), _ptr(g), _ptr(h), _ptr(initial_state), _ptr(grad_h), _ptr(grad_final_state), _ptr(cu_seqlens),
+            seqs, _ptr(out["dx"]), _ptr(out["dg"]), _ptr(out["dS0"]))
+    _scan_run("kda_scan_backward", grad_h.device, stream, args, (B, T, D), code, prep, input_gate, seqs, workspace, made)
+    return out
+
+
+def kda_scan_backward_ckpt(checkpoint, grad_h, grad_final_state=None, *, cu_seqlens=None,
+                           input_gate=KDA_SCAN_INPUT_PLAIN, prep=0, workspace=None, stream=None,
+                           want_initial_state_grad=True):
+    """kda_scan_backward from the 8-bit checkpoint that kda_scan_fwd filled (same sizes, ``prep``, ``input_gate``
+    and ``cu_seqlens``) in place of x, g, h and the initial state."""
+    _check_dev("grad_h", grad_h)
+    code = _dtype_code(grad_h.dtype)
+    B, T, D, seqs = _scan_check(grad_h.device, grad_h.shape, grad_h.dtype, cu_seqlens, {},
+                                {"grad_final_state": grad_final_state})
+    _check_ckpt(checkpoint, grad_h.shape, grad_h.device)
+    made = []
+    out = _scan_grads(grad_h, seqs, want_initial_state_grad, made)
+    args = (_ptr(checkpoint), _ptr(grad_h), _ptr(grad_final_state), _ptr(cu_seqlens), seqs, _ptr(out["dx"]),
+            _ptr(out["dg"]), _ptr(out["dS0"]))
+    _scan_run("kda_scan_backward_ckpt", grad_h.device, stream, args, (B, T, D), code, prep, input_gate, seqs, workspace,
+              made)
+    return out
+
+
+def kda_scan_step(x, g, state, *, input_gate=KDA_SCAN_INPUT_PLAIN, prep=0, h=None, out_state=None, stream=None):
+    """One token of the elementwise recurrence for N sequences: x, g [N,D], state [N,D] fp32, updated in place, or
+    left and the new one written to ``out_state``.  Returns h [N,D] in the input dtype."""
+    _check_dev("x", x)
+    code = _dtype_code(x.dtype)
+    if x.dim() != 2:
+        raise ValueError("x must be [N,D]")
+    out_state = state if out_state is None else out_state
+    made = []
+    if h is None:
+        h = torch.empty_like(x)
+        made.append(h)
+    for name, t, dtype in (("g", g, x.dtype), ("state", state, torch.float32), ("out_state", out_state, torch.float32),
+                           ("h", h, x.dtype)):
+        _check_dev(name, t, dtype)
+        if t.shape != x.shape or t.device != x.device:
+            raise ValueError(f"{name} must be {list(x.shape)} on {x.device}")
+    with _on(x.device):
+        st = load().kda_scan_step(_ptr(x), _ptr(g), _ptr(state), _ptr(out_state), _ptr(h), x.shape[0], x.shape[1],
+                                  code, int(prep), int(input_gate), _stream(stream, x.device))
+    _record(made, stream, x.device)
+    if st != KDA_OK:
+        raise KDAError(st, "kda_scan_step")
+    return h

@@ -317,4 +317,169 @@ kda_status kda_recurrent_step_ex(const void* q, const void* k, const void* v, co
   return recurrent_step_impl(q, k, v, g, beta, scale, state, o, N, H, dk, dv, dtype, gate, prep, stream);
 }
 
+// ------------------------------------------------ elementwise gated linear recurrence
+
+// Sizes the scan entry points take: B, T, N >= 0, D >= 1, at most 2^40
+// elements (so that byte counts cannot wrap).  Returns the status they give.
+static kda_status scan_sizes(int64_t B, int64_t T, int64_t D, int64_t N, int dtype) {
+  if (B < 0 || T < 0 || D < 1 || N < 0) return KDA_ERR_INVALID_ARG;
+  if (dtype != KDA_F32 && dtype != KDA_BF16) return KDA_ERR_INVALID_ARG;
+  constexpr int64_t kMost = (int64_t)1 << 40;
+  if (B * D > kMost || N * D > kMost || (T > 0 && B * D > kMost / T)) return KDA_ERR_UNSUPPORTED;
+  return KDA_OK;
+}
+
+size_t kda_scan_workspace_size(int B, int T, int D, int num_seqs, int dtype) {
+  if (scan_sizes(B, T, D, num_seqs, dtype) != KDA_OK || (num_seqs > 0 && B != 1)) return 0;
+  return kda::scan_workspace_bytes(B, T, D, num_seqs, dtype);
+}
+
+size_t kda_scan_checkpoint_size(int B, int T, int D) {
+  if (scan_sizes(B, T, D, 0, KDA_BF16) != KDA_OK) return 0;
+  return kda::scan_ckpt_layout((size_t)B * T, D).total;
+}
+
+// What the three sequence calls share: sizes, flags, the buffers (each with
+// whether it must be given), overlaps, workspace.
+static kda_status scan_checks(const kda::ScanArgs& a, const Range* in, int n_in, const Range* out,
+                              int n_out, const Range* need, int n_need, void* workspace, size_t workspace_bytes) {
+  for (int i = 0; i < n_need; ++i)
+    if (need[i].bytes && !need[i].lo) return KDA_ERR_INVALID_ARG;
+  for (int i = 0; i < n_in; ++i)
+    if (in[i].lo && !aligned16(in[i].lo) && (const void*)in[i].lo != (const void*)a.cu) return KDA_ERR_INVALID_ARG;
+  for (int i = 0; i < n_out; ++i) {
+    if (out[i].lo && !aligned16(out[i].lo)) return KDA_ERR_INVALID_ARG;
+    for (int j = 0; j < n_in; ++j) {
+      // the forward's final state may take the initial state's place
+      if (out[i].lo == (const char*)a.sT && in[j].lo == (const char*)a.s0 && a.sT == a.s0 && !a.dy) continue;
+      if (overlaps(out[i], in[j])) return KDA_ERR_INVALID_ARG;
+    }
+    for (int j = i + 1; j < n_out; ++j)
+      if (overlaps(out[i], out[j])) return KDA_ERR_INVALID_ARG;
+  }
+  const size_t need_ws = kda::scan_workspace_bytes(a.B, a.T, a.D, a.N, a.dtype);
+  if (need_ws) {
+    if (!workspace || workspace_bytes < need_ws || (reinterpret_cast<uintptr_t>(workspace) & 255u))
+      return KDA_ERR_INVALID_ARG;
+    const Range rw{(const char*)workspace, workspace_bytes};
+    for (int i = 0; i < n_in; ++i)
+      if (overlaps(rw, in[i])) return KDA_ERR_INVALID_ARG;
+    for (int i = 0; i < n_out; ++i)
+      if (overlaps(rw, out[i])) return KDA_ERR_INVALID_ARG;
+  }
+  return KDA_OK;
+}
+
+static kda_status scan_flags(int64_t B, int64_t T, int64_t D, const int32_t* cu, int64_t num_seqs, int dtype, int prep,
+                             int input_gate) {
+  const kda_status st = scan_sizes(B, T, D, cu ? num_seqs : 0, dtype);
+  if (st != KDA_OK) return st;
+  if (prep & ~KDA_PREP_GATE_LOGSIGMOID) return KDA_ERR_INVALID_ARG;
+  if (input_gate != KDA_SCAN_INPUT_PLAIN && input_gate != KDA_SCAN_INPUT_COMPLEMENT) return KDA_ERR_INVALID_ARG;
+  if (cu && (B != 1 || num_seqs < 1 || !aligned_to(cu, 4))) return KDA_ERR_INVALID_ARG;
+  return KDA_OK;
+}
+
+// No rows: the state passes through unchanged.
+static kda_status scan_empty(const float* from, float* to, size_t bytes, cudaStream_t stream) {
+  if (!to || !bytes || from == to) return KDA_OK;
+  return from_cuda(from ? cudaMemcpyAsync(to, from, bytes, cudaMemcpyDeviceToDevice, stream)
+                        : cudaMemsetAsync(to, 0, bytes, stream));
+}
+
+kda_status kda_scan_fwd(const void* x, const void* g, const float* initial_state, const int32_t* cu_seqlens,
+                        int num_seqs, void* h, float* final_state, void* checkpoint, int B, int T, int D, int dtype,
+                        int prep, int input_gate, void* workspace, size_t workspace_bytes, void* stream_) {
+  cudaStream_t stream = static_cast<cudaStream_t>(stream_);
+  kda_status st = scan_flags(B, T, D, cu_seqlens, num_seqs, dtype, prep, input_gate);
+  if (st != KDA_OK) return st;
+  const int N = cu_seqlens ? num_seqs : 0;
+  const size_t nb = (size_t)B * T * D * elem_bytes(dtype), sb = (size_t)(N ? N : B) * D * sizeof(float);
+  kda::ScanArgs a{};
+  a.x = x, a.g = g, a.s0 = initial_state, a.cu = cu_seqlens, a.out = h, a.sT = final_state;
+  a.ckpt = static_cast<uint8_t*>(checkpoint);
+  a.B = B, a.T = T, a.D = D, a.N = N, a.dtype = dtype, a.prep = prep, a.complement = input_gate;
+  const Range in[] = {{(const char*)x, nb}, {(const char*)g, nb}, {(const char*)initial_state, sb},
+                      {(const char*)cu_seqlens, (size_t)(N + 1) * 4}};
+  const Range out[] = {{(const char*)h, nb}, {(const char*)final_state, sb},
+                       {(const char*)checkpoint, kda::scan_ckpt_layout((size_t)B * T, D).total}};
+  const Range need[] = {in[0], in[1], out[0]};
+  st = scan_checks(a, in, 4, out, 3, need, 3, workspace, workspace_bytes);
+  if (st != KDA_OK) return st;
+  if (B == 0 || T == 0) return scan_empty(initial_state, final_state, sb, stream);
+  return from_cuda(kda::launch_scan_fwd(a, workspace, stream));
+}
+
+kda_status kda_scan_backward(const void* x, const void* g, const void* h, const float* initial_state,
+                             const void* grad_h, const float* grad_final_state, const int32_t* cu_seqlens,
+                             int num_seqs, void* grad_x, void* grad_g, float* grad_initial_state, int B, int T, int D,
+                             int dtype, int prep, int input_gate, void* workspace, size_t workspace_bytes,
+                             void* stream_) {
+  cudaStream_t stream = static_cast<cudaStream_t>(stream_);
+  kda_status st = scan_flags(B, T, D, cu_seqlens, num_seqs, dtype, prep, input_gate);
+  if (st != KDA_OK) return st;
+  const int N = cu_seqlens ? num_seqs : 0;
+  const size_t nb = (size_t)B * T * D * elem_bytes(dtype), sb = (size_t)(N ? N : B) * D * sizeof(float);
+  kda::ScanArgs a{};
+  a.x = input_gate == KDA_SCAN_INPUT_COMPLEMENT ? x : nullptr;
+  a.g = g, a.h = h, a.dy = grad_h, a.s0 = grad_final_state, a.h0 = initial_state, a.cu = cu_seqlens;
+  a.out = grad_x, a.dg = grad_g, a.sT = grad_initial_state;
+  a.B = B, a.T = T, a.D = D, a.N = N, a.dtype = dtype, a.prep = prep, a.complement = input_gate;
+  const Range in[] = {{(const char*)a.x, nb}, {(const char*)g, nb}, {(const char*)h, nb}, {(const char*)grad_h, nb},
+                      {(const char*)initial_state, sb}, {(const char*)grad_final_state, sb},
+                      {(const char*)cu_seqlens, (size_t)(N + 1) * 4}};
+  const Range out[] = {{(const char*)grad_x, nb}, {(const char*)grad_g, nb}, {(const char*)grad_initial_state, sb}};
+  const Range need[] = {in[1], in[2], in[3], out[0], out[1],
+                        {(const char*)a.x, input_gate == KDA_SCAN_INPUT_COMPLEMENT ? nb : 0}};
+  st = scan_checks(a, in, 7, out, 3, need, 6, workspace, workspace_bytes);
+  if (st != KDA_OK) return st;
+  if (B == 0 || T == 0) return scan_empty(grad_final_state, grad_initial_state, sb, stream);
+  return from_cuda(kda::launch_scan_bwd(a, workspace, stream));
+}
+
+kda_status kda_scan_backward_ckpt(const void* checkpoint, const void* grad_h, const float* grad_final_state,
+                                  const int32_t* cu_seqlens, int num_seqs, void* grad_x, void* grad_g,
+                                  float* grad_initial_state, int B, int T, int D, int dtype, int prep, int input_gate,
+                                  void* workspace, size_t workspace_bytes, void* stream_) {
+  cudaStream_t stream = static_cast<cudaStream_t>(stream_);
+  kda_status st = scan_flags(B, T, D, cu_seqlens, num_seqs, dtype, prep, input_gate);
+  if (st != KDA_OK) return st;
+  const int N = cu_seqlens ? num_seqs : 0;
+  const size_t nb = (size_t)B * T * D * elem_bytes(dtype), sb = (size_t)(N ? N : B) * D * sizeof(float);
+  kda::ScanArgs a{};
+  a.dy = grad_h, a.s0 = grad_final_state, a.cu = cu_seqlens, a.out = grad_x, a.dg = grad_g, a.sT = grad_initial_state;
+  a.ckpt = static_cast<uint8_t*>(const_cast<void*>(checkpoint));
+  a.B = B, a.T = T, a.D = D, a.N = N, a.dtype = dtype, a.prep = prep, a.complement = input_gate;
+  const Range in[] = {{(const char*)checkpoint, kda::scan_ckpt_layout((size_t)B * T, D).total},
+                      {(const char*)grad_h, nb}, {(const char*)grad_final_state, sb},
+                      {(const char*)cu_seqlens, (size_t)(N + 1) * 4}};
+  const Range out[] = {{(const char*)grad_x, nb}, {(const char*)grad_g, nb}, {(const char*)grad_initial_state, sb}};
+  const Range need[] = {in[0], in[1], out[0], out[1]};
+  st = scan_checks(a, in, 4, out, 3, need, 4, workspace, workspace_bytes);
+  if (st != KDA_OK) return st;
+  if (B == 0 || T == 0) return scan_empty(grad_final_state, grad_initial_state, sb, stream);
+  return from_cuda(kda::launch_scan_bwd(a, workspace, stream));
+}
+
+kda_status kda_scan_step(const void* x, const void* g, const float* state, float* out_state, void* h, int N, int D,
+                         int dtype, int prep, int input_gate, void* stream_) {
+  const kda_status st = scan_flags(N, 1, D, nullptr, 0, dtype, prep, input_gate);
+  if (st != KDA_OK) return st;
+  if (N == 0) return KDA_OK;
+  const size_t n = (size_t)N * D, nb = n * elem_bytes(dtype);
+  const Range in[] = {{(const char*)x, nb}, {(const char*)g, nb}, {(const char*)state, n * 4}};
+  const Range out[] = {{(const char*)out_state, n * 4}, {(const char*)h, nb}};
+  for (Range r : in)
+    if (!r.lo || !aligned16(r.lo)) return KDA_ERR_INVALID_ARG;
+  for (Range r : out) {
+    if (!r.lo || !aligned16(r.lo)) return KDA_ERR_INVALID_ARG;
+    for (Range q : in)
+      if (!(r.lo == (const char*)out_state && q.lo == (const char*)state && out_state == state) && overlaps(r, q))
+        return KDA_ERR_INVALID_ARG;
+  }
+  if (overlaps(out[0], out[1])) return KDA_ERR_INVALID_ARG;
+  return from_cuda(kda::launch_scan_step(x, g, state, out_state, h, n, dtype, prep, input_gate,
+                                         static_cast<cudaStream_t>(stream_)));
+}
+
 }  // extern "C"

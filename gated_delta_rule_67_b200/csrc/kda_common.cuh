@@ -113,6 +113,41 @@ __device__ __forceinline__ float gate_alpha(int gate, int prep, const T* g_chan,
   return 1.f;
 }
 
+// Elementwise gated linear recurrence (kda_scan.cu).  Pointers not used by a
+// call are null; `ckpt` is written by the forward and read by the backward.
+struct ScanArgs {
+  const void *x, *g, *h, *dy;       // inputs (dtype)
+  const float* s0;                  // initial state, or dL/d final state in the backward (null: zeros)
+  const float* h0;                  // backward: the forward's initial state (null: zeros)
+  const int32_t* cu;                // packed sequences, or null
+  void *out, *dg;                   // h or dL/dx, and dL/dg (dtype)
+  float* sT;                        // final state, or dL/d initial state (null: skipped)
+  uint8_t* ckpt;                    // 8-bit checkpoint, or null
+  int B, T, D, N;                   // N: packed sequences (0 without cu)
+  int dtype, prep, complement;
+};
+// Parts of the checkpoint (byte offsets) for `rows` rows of D channels.
+struct ScanCkptLayout {
+  size_t pitch, blocks;             // code bytes per row; blocks of 128 channels
+  size_t z, lam_scale, z_scale, total;
+};
+inline __host__ __device__ ScanCkptLayout scan_ckpt_layout(size_t rows, int D) {
+  ScanCkptLayout l;
+  l.pitch = ((size_t)D + 15) / 16 * 16;
+  l.blocks = ((size_t)D + 127) / 128;
+  const size_t codes = (rows * l.pitch + 255) / 256 * 256, scales = (rows * l.blocks + 255) / 256 * 256;
+  l.z = codes;
+  l.lam_scale = 2 * codes;
+  l.z_scale = 2 * codes + scales;
+  l.total = 2 * (codes + scales);
+  return l;
+}
+size_t scan_workspace_bytes(int B, int T, int D, int N, int dtype);
+cudaError_t launch_scan_fwd(const ScanArgs& a, void* ws, cudaStream_t stream);
+cudaError_t launch_scan_bwd(const ScanArgs& a, void* ws, cudaStream_t stream);
+cudaError_t launch_scan_step(const void* x, const void* g, const float* state, float* out_state, void* h, size_t n,
+                             int dtype, int prep, int complement, cudaStream_t stream);
+
 // Records events[i] on the stream when an events array was given.
 inline cudaError_t mark(void* const* events, int i, cudaStream_t stream) {
   return events ? cudaEventRecord(static_cast<cudaEvent_t>(events[i]), stream) : cudaSuccess;

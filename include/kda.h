@@ -341,6 +341,117 @@ KDA_API kda_status kda_recurrent_step_ex(const void* q, const void* k, const voi
                                          const void* beta, float scale, float* state, void* o, int N, int H,
                                          int dk, int dv, int dtype, int gate, int prep, void* stream);
 
+/*
+ * ---------------------------------------------------------------------------
+ * Elementwise gated linear recurrence: the family's vector-state member, one
+ * scalar state per channel (no key / value products),
+ *
+ *     h_t = alpha_t h_{t-1} + w_t x_t,     alpha_t = exp(lambda_t)
+ *
+ * lambda_t is the log-gate: `g` itself, or log sigmoid(g) with the prep bit
+ * KDA_PREP_GATE_LOGSIGMOID (the only bit these calls take).  The input weight
+ * w_t is chosen by `input_gate` (kda_scan_input): 1, or 1 - alpha_t, which
+ * makes h a weighted mean of its inputs.  The pages describe no such operator;
+ * it has no counterpart there.
+ *
+ * Layout: x, g, h and their gradients are [B, T, D] (dtype, contiguous, any
+ * D >= 1); initial_state and final_state are [B, D] fp32.  State, sums and
+ * products are fp32; h and the gradients are rounded once.
+ *
+ * Packed sequences: with `cu_seqlens` non-NULL (device, int32,
+ * [num_seqs + 1]), B must be 1, sequence i owns the rows
+ * cu_seqlens[i] <= t < cu_seqlens[i + 1] of the T rows, and the states are
+ * [num_seqs, D].  Nothing passes from one sequence to another, not even an
+ * infinity or NaN.  An empty sequence's final state is its initial state.
+ * Rows outside every sequence are not read; they get zeros in h and the
+ * gradients.  The values must be non-decreasing and within [0, T]; they are
+ * not checked (they live on the device): others give meaningless results, but
+ * no access outside the buffers.  With cu_seqlens NULL, num_seqs is ignored.
+ */
+typedef enum { KDA_SCAN_INPUT_PLAIN = 0, KDA_SCAN_INPUT_COMPLEMENT = 1 } kda_scan_input;
+
+/*
+ * Bytes of device workspace kda_scan_fwd, kda_scan_backward and
+ * kda_scan_backward_ckpt need (0 if none, and for arguments they reject).
+ * `num_seqs`: the number of packed sequences, 0 without cu_seqlens.
+ */
+KDA_API size_t kda_scan_workspace_size(int B, int T, int D, int num_seqs, int dtype);
+
+/*
+ * Bytes of the 8-bit activation checkpoint of B x T rows of D channels (0 for
+ * bad sizes): two bytes and a little per element, against four (fp32: eight)
+ * for the activations it stands for, six (twelve) with KDA_SCAN_INPUT_COMPLEMENT.
+ *
+ * It holds all that the backward multiplies: lambda_t, and
+ * z_t = h_{t-1} (PLAIN) or h_{t-1} - x_t (COMPLEMENT), the factor of
+ * d alpha_t; z of a sequence's first row contains its initial state.  Each is
+ * e4m3 with one power-of-two scale 2^k per row and block of 128 channels
+ * (channels 128 j .. 128 j + 127), k the least integer >= -126 for which the
+ * block's largest finite magnitude is at most 448 * 2^k.  A code stands for
+ * e4m3(code) * 2^k; values are rounded to nearest even from fp32, infinities
+ * and NaN become NaN.  With R = B * T rows, P = D rounded up to 16,
+ * K = ceil(D / 128), the parts follow each other, each from a multiple of 256
+ * bytes: lambda codes [R][P], z codes [R][P], lambda scales [K][R], z scales
+ * [K][R] (bytes, k + 127).  Channels D .. P - 1 of the codes are undefined.
+ * Rows outside every packed sequence hold zeros.
+ */
+KDA_API size_t kda_scan_checkpoint_size(int B, int T, int D);
+
+/*
+ * The recurrence over T rows.
+ *   initial_state : NULL for zeros
+ *   final_state   : NULL to skip; may be initial_state's buffer
+ *   checkpoint    : NULL, or kda_scan_checkpoint_size() bytes, 16-byte
+ *                   aligned, written beside h
+ *   workspace     : kda_scan_workspace_size() bytes, 256-byte aligned,
+ *                   contents on entry do not matter; not shared by two calls
+ *                   in flight (two captured graphs among them).  Its header is
+ *                   read by kda_chunk_fwd_check: KDA_ERR_TIMEOUT if a bounded
+ *                   wait inside the kernel gave up (outputs not valid).
+ * Results do not depend on the order in which the GPU runs the blocks.
+ * B = 0 or T = 0 is valid: the final state is the initial state.
+ */
+KDA_API kda_status kda_scan_fwd(const void* x, const void* g, const float* initial_state, const int32_t* cu_seqlens,
+                                int num_seqs, void* h, float* final_state, void* checkpoint, int B, int T, int D,
+                                int dtype, int prep, int input_gate, void* workspace, size_t workspace_bytes,
+                                void* stream);
+
+/*
+ * Gradients of a loss through kda_scan_fwd, given dL/dh and dL/d final_state
+ * (NULL: zeros) and the forward's x, g, h and initial_state (x is read only
+ * for KDA_SCAN_INPUT_COMPLEMENT, else NULL is allowed):
+ *     d_t = dL/dh_t + alpha_{t+1} d_{t+1}    (+ dL/d final_state in the last row)
+ *     dL/dx_t = w_t d_t,   dL/dlambda_t = alpha_t d_t z_t,   dL/dS_0 = alpha_1 d_1
+ * with z as in the checkpoint; grad_g is dL/dlambda_t, times 1 - alpha_t with
+ * KDA_PREP_GATE_LOGSIGMOID.  h is read as the forward stored it (rounded to
+ * dtype).  grad_initial_state may be NULL.  Outputs must not overlap any other
+ * buffer.  Workspace and packed sequences as kda_scan_fwd.
+ */
+KDA_API kda_status kda_scan_backward(const void* x, const void* g, const void* h, const float* initial_state,
+                                     const void* grad_h, const float* grad_final_state, const int32_t* cu_seqlens,
+                                     int num_seqs, void* grad_x, void* grad_g, float* grad_initial_state, int B, int T,
+                                     int D, int dtype, int prep, int input_gate, void* workspace,
+                                     size_t workspace_bytes, void* stream);
+
+/*
+ * kda_scan_backward from the 8-bit checkpoint that kda_scan_fwd wrote with the
+ * same sizes, prep, input_gate and cu_seqlens, in place of x, g, h and the
+ * initial state: the same formulas with lambda and z as the checkpoint holds
+ * them.  dtype is the type of grad_h, grad_x and grad_g.
+ */
+KDA_API kda_status kda_scan_backward_ckpt(const void* checkpoint, const void* grad_h, const float* grad_final_state,
+                                          const int32_t* cu_seqlens, int num_seqs, void* grad_x, void* grad_g,
+                                          float* grad_initial_state, int B, int T, int D, int dtype, int prep,
+                                          int input_gate, void* workspace, size_t workspace_bytes, void* stream);
+
+/*
+ * One token for N sequences: out_state = alpha state + w x (fp32, [N, D]), h
+ * the same rounded to dtype.  x, g, h: [N, D].  out_state may be state's
+ * buffer (updated in place), else must not overlap it.
+ */
+KDA_API kda_status kda_scan_step(const void* x, const void* g, const float* state, float* out_state, void* h, int N,
+                                 int D, int dtype, int prep, int input_gate, void* stream);
+
 #ifdef __cplusplus
 }
 #endif
