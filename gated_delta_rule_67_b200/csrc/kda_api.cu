@@ -320,12 +320,14 @@ kda_status kda_recurrent_step_ex(const void* q, const void* k, const void* v, co
 // ------------------------------------------------ elementwise gated linear recurrence
 
 // Sizes the scan entry points take: B, T, N >= 0, D >= 1, at most 2^40
-// elements (so that byte counts cannot wrap).  Returns the status they give.
+// elements (so that byte counts cannot wrap), 2^31 - 1 tiles of 32 rows x 128
+// channels and 2^28 packed sequences.  Returns the status they give.
 static kda_status scan_sizes(int64_t B, int64_t T, int64_t D, int64_t N, int dtype) {
   if (B < 0 || T < 0 || D < 1 || N < 0) return KDA_ERR_INVALID_ARG;
   if (dtype != KDA_F32 && dtype != KDA_BF16) return KDA_ERR_INVALID_ARG;
   constexpr int64_t kMost = (int64_t)1 << 40;
   if (B * D > kMost || N * D > kMost || (T > 0 && B * D > kMost / T)) return KDA_ERR_UNSUPPORTED;
+  if (B * ((D + 127) / 128) * ((T + 31) / 32) > INT32_MAX || N > (1 << 28)) return KDA_ERR_UNSUPPORTED;
   return KDA_OK;
 }
 
@@ -350,8 +352,9 @@ static kda_status scan_checks(const kda::ScanArgs& a, const Range* in, int n_in,
   for (int i = 0; i < n_out; ++i) {
     if (out[i].lo && !aligned16(out[i].lo)) return KDA_ERR_INVALID_ARG;
     for (int j = 0; j < n_in; ++j) {
-      // the forward's final state may take the initial state's place
-      if (out[i].lo == (const char*)a.sT && in[j].lo == (const char*)a.s0 && a.sT == a.s0 && !a.dy) continue;
+      // the forward's final state may take the initial state's place (the checkpoint's z
+      // reads the initial state when other blocks may already write the final one)
+      if (out[i].lo == (const char*)a.sT && in[j].lo == (const char*)a.s0 && a.sT == a.s0 && !a.dy && !a.ckpt) continue;
       if (overlaps(out[i], in[j])) return KDA_ERR_INVALID_ARG;
     }
     for (int j = i + 1; j < n_out; ++j)

@@ -2,19 +2,55 @@
 //
 //     h_t = alpha_t h_{t-1} + w_t x_t,   alpha_t = exp(lambda_t),   w_t = 1 or 1 - alpha_t
 //
-// lambda_t is the given log-gate or log sigmoid of a raw projection.  One
-// thread per channel walks its sequence; a block holds 128 channels, which
-// are one scale block of the 8-bit checkpoint.
+// lambda_t is the given log-gate or log sigmoid of a raw projection.
+//
+// Mathematics.  A stretch of rows maps the state that enters it to the one
+// that leaves it by c -> A c + Bs per channel, A the product of its alpha and
+// Bs its end state from zero; stretches compose: (A2, B2) after (A1, B1) is
+// (A1 A2, A2 B1 + B2).  The backward is the same recurrence down the rows, on
+// c_t = alpha_t d_t with d_t = dL/dh_t + c_{t+1}.  The first row of a sequence
+// (backward: the last) takes the sequence's own initial state (final
+// gradient); its stretch is marked as not depending on what enters it
+// (A = -0, which no product of alpha >= 0 gives), so that nothing passes from
+// one sequence to the next, NaN included.
+//
+// What bounds it: bytes.  bf16 forward 6 B per element, backward 10-12, from
+// the 8-bit checkpoint 8.  So the data is read once, in one pass: a tile is
+// 128 channels (one scale block of the checkpoint) x L rows; each of 8 warps
+// holds R = L / 8 rows x 128 channels of a tile as alpha and input in
+// registers, folds them to (A, Bs), and the 8 pairs are joined through shared
+// memory.  Tiles of one (sequence batch, channel block) chain are joined in
+// the order of the rows: each tile publishes its (A, Bs), the last of each
+// group of kGroup tiles the state that leaves the group; a tile folds the
+// pairs of its group's earlier tiles onto the state that left the group
+// before.  The order of the fold is fixed, so the bits are the same every
+// time.  Tiles are drawn by ticket in the order of the rows, so whatever a
+// tile waits for belongs to a block that is running; the words of the pairs
+// are their own flags (all bits set = not yet written), so one trip to L2
+// sees and fetches them.  A producer warp draws tickets and feeds the next
+// tiles by TMA while the current one is computed.
+#include <cudaTypedefs.h>
 #include <cuda_fp8.h>
 
+#include <algorithm>
+#include <atomic>
 #include <type_traits>
 
 #include "kda_common.cuh"
+#include "sm100.cuh"
 
 namespace kda {
 namespace {
 
-constexpr int kBlock = 128;  // channels per scale of the checkpoint, and threads per block
+using namespace sm100;
+constexpr int kBlock = 128;     // channels per tile and per scale of the checkpoint
+constexpr int kWarps = 8;       // consumer warps of a tile; one more feeds them
+constexpr int kGroup = 16;      // tiles whose pairs are folded before a state is published
+constexpr int kStages = 2;
+constexpr int kInOrderRows = 256;  // chains of so few rows are walked by one block each
+constexpr uint32_t kEmpty = 0xffffffffu;     // a word not yet written
+constexpr uint32_t kPollLimit = 1u << 22;    // polls before a wait gives up
+constexpr uint32_t kBarLimit = 1u << 22;
 
 // alpha and 1 - alpha, each to a few ulp on its own (1 - alpha by subtraction
 // would lose the small rates that make the long memories), and, where asked
@@ -31,9 +67,6 @@ __device__ __forceinline__ void gate(float g, float& alpha, float& beta) {
   }
 }
 
-template <typename T>
-__device__ __forceinline__ float load(const T* p, size_t i) { return to_f32(__ldg(p + i)); }
-
 // ---------------------------------------------------------------- checkpoint
 // k + 127 of the scale 2^k: the least k >= -126 with top <= 448 * 2^k, for
 // top >= 0 finite.  top = m 2^e with 1 <= m < 2; 448 = 1.75 * 2^8.
@@ -47,141 +80,601 @@ __device__ __forceinline__ uint32_t magnitude(float v) {  // for the block's max
   const uint32_t b = __float_as_uint(v) & 0x7fffffffu;
   return b < 0x7f800000u ? b : 0u;
 }
-__device__ __forceinline__ uint8_t encode(float v, float inv) {
-  v = fabsf(v) <= 3.402823466e38f ? v * inv : __int_as_float(0x7fffffff);
-  return (uint8_t)__nv_cvt_float_to_fp8(v, __NV_SATFINITE, __NV_E4M3);
+__device__ __forceinline__ bool finite(float v) { return fabsf(v) <= 3.402823466e38f; }
+// Four values as e4m3 of v * inv (inv a power of two; non-finite values give NaN).
+__device__ __forceinline__ uint32_t encode4(const float* v, float inv) {
+  float q[4];
+#pragma unroll
+  for (int j = 0; j < 4; ++j) q[j] = finite(v[j]) ? v[j] * inv : __int_as_float(0x7fffffff);
+  const uint32_t lo = __nv_cvt_float2_to_fp8x2(make_float2(q[0], q[1]), __NV_SATFINITE, __NV_E4M3);
+  const uint32_t hi = __nv_cvt_float2_to_fp8x2(make_float2(q[2], q[3]), __NV_SATFINITE, __NV_E4M3);
+  return lo | hi << 16;
 }
-__device__ __forceinline__ float decode(uint8_t c, float scale) {
-  return __half2float(__half(__nv_cvt_fp8_to_halfraw(c, __NV_E4M3))) * scale;
-}
-
-// The block's maximum magnitude (bits), over its 128 threads.
-__device__ __forceinline__ uint32_t block_max(uint32_t v, uint32_t* buf) {
-  v = __reduce_max_sync(0xffffffffu, v);
-  __syncthreads();
-  if ((threadIdx.x & 31) == 0) buf[threadIdx.x >> 5] = v;
-  __syncthreads();
-  return max(max(buf[0], buf[1]), max(buf[2], buf[3]));
-}
-
-// The rows [lo, hi) of sequence s, clamped to the buffer.
-__device__ __forceinline__ void rows_of(const ScanArgs& a, int s, int64_t& lo, int64_t& hi) {
-  if (a.cu) {
-    lo = min(max(__ldg(a.cu + s), 0), a.T);
-    hi = min(max(__ldg(a.cu + s + 1), 0), a.T);
-  } else {
-    lo = (int64_t)s * a.T;
-    hi = lo + a.T;
-  }
+__device__ __forceinline__ void decode4(uint32_t c, float scale, float* v) {
+  const __half2 a = __half2(__nv_cvt_fp8x2_to_halfraw2((__nv_fp8x2_storage_t)(c & 0xffffu), __NV_E4M3));
+  const __half2 b = __half2(__nv_cvt_fp8x2_to_halfraw2((__nv_fp8x2_storage_t)(c >> 16), __NV_E4M3));
+  const float2 x = __half22float2(a), y = __half22float2(b);
+  v[0] = x.x * scale, v[1] = x.y * scale, v[2] = y.x * scale, v[3] = y.y * scale;
 }
 
-// Zeros in the rows that no sequence owns (packed only).
+
+// ------------------------------------------------------------ four channels
 template <typename IO>
-__device__ void zero_rows(const ScanArgs& a, int c, int64_t lo, int64_t hi) {
-  const ScanCkptLayout l = scan_ckpt_layout((size_t)a.B * a.T, a.D);
-  for (int64_t t = lo; t < hi; ++t) {
-    if (c < a.D) {
-      static_cast<IO*>(a.out)[(size_t)t * a.D + c] = from_f32<IO>(0.f);
-      if (a.dg) static_cast<IO*>(a.dg)[(size_t)t * a.D + c] = from_f32<IO>(0.f);
-      if (a.ckpt && !a.dy) a.ckpt[t * l.pitch + c] = a.ckpt[l.z + t * l.pitch + c] = 0;
+__device__ __forceinline__ void lds4(const uint8_t* p, float* v) {
+  if constexpr (sizeof(IO) == 4) {
+    const float4 q = *reinterpret_cast<const float4*>(p);
+    v[0] = q.x, v[1] = q.y, v[2] = q.z, v[3] = q.w;
+  } else {
+    const uint2 q = *reinterpret_cast<const uint2*>(p);
+    v[0] = __uint_as_float(q.x << 16), v[1] = __uint_as_float(q.x & 0xffff0000u);
+    v[2] = __uint_as_float(q.y << 16), v[3] = __uint_as_float(q.y & 0xffff0000u);
+  }
+}
+template <typename IO>
+__device__ __forceinline__ void stg4(IO* p, const float* v, int n, bool vec) {
+  if (vec) {
+    if (n <= 0) return;
+    if constexpr (sizeof(IO) == 4) {
+      __stcs(reinterpret_cast<float4*>(p), make_float4(v[0], v[1], v[2], v[3]));
+    } else {
+      const __nv_bfloat162 a = __floats2bfloat162_rn(v[0], v[1]), b = __floats2bfloat162_rn(v[2], v[3]);
+      __stcs(reinterpret_cast<uint2*>(p),
+             make_uint2(*reinterpret_cast<const uint32_t*>(&a), *reinterpret_cast<const uint32_t*>(&b)));
     }
-    if (a.ckpt && !a.dy && threadIdx.x == 0) {
-      const size_t at = (size_t)blockIdx.x * a.B * a.T + t;
-      a.ckpt[l.lam_scale + at] = a.ckpt[l.z_scale + at] = 1;
-    }
+  } else {
+#pragma unroll
+    for (int j = 0; j < 4; ++j)
+      if (j < n) p[j] = from_f32<IO>(v[j]);
+  }
+}
+__device__ __forceinline__ void ldg4(const float* p, float* v, int n, bool vec) {
+#pragma unroll
+  for (int j = 0; j < 4; ++j) v[j] = 0.f;
+  if (!p || n <= 0) return;
+  if (vec) {
+    const float4 q = *reinterpret_cast<const float4*>(p);
+    v[0] = q.x, v[1] = q.y, v[2] = q.z, v[3] = q.w;
+  } else {
+#pragma unroll
+    for (int j = 0; j < 4; ++j)
+      if (j < n) v[j] = p[j];
   }
 }
 
-template <typename IO, bool RAW, bool COMPL>
-__global__ void __launch_bounds__(kBlock) scan_fwd_kernel(const ScanArgs a) {
-  __shared__ uint32_t red[2][4];
-  const int c = blockIdx.x * kBlock + threadIdx.x, nseq = a.cu ? a.N : a.B;
-  const bool live = c < a.D;
-  const size_t rows = (size_t)a.B * a.T;
-  const ScanCkptLayout l = scan_ckpt_layout(rows, a.D);
-  for (int s = blockIdx.y; s < nseq; s += gridDim.y) {
-    int64_t lo, hi;
-    rows_of(a, s, lo, hi);
-    const size_t st = (size_t)s * a.D + c;
-    float h = live && a.s0 ? a.s0[st] : 0.f;
-    for (int64_t t = lo; t < hi; ++t) {
-      const size_t at = (size_t)t * a.D + c;
-      const float g = live ? load(static_cast<const IO*>(a.g), at) : 0.f;
-      const float x = live ? load(static_cast<const IO*>(a.x), at) : 0.f;
-      float alpha, beta;
-      gate<RAW>(g, alpha, beta);
-      if (a.ckpt) {
-        const float lam = RAW ? log_sigmoid(g) : g, z = COMPL ? h - x : h;
-        const int kl = scale_code(__uint_as_float(block_max(live ? magnitude(lam) : 0u, red[0])));
-        const int kz = scale_code(__uint_as_float(block_max(live ? magnitude(z) : 0u, red[1])));
-        if (live) {
-          a.ckpt[t * l.pitch + c] = encode(lam, pow2(254 - kl));
-          a.ckpt[l.z + t * l.pitch + c] = encode(z, pow2(254 - kz));
-        }
-        if (threadIdx.x == 0) {
-          a.ckpt[l.lam_scale + blockIdx.x * rows + t] = (uint8_t)kl;
-          a.ckpt[l.z_scale + blockIdx.x * rows + t] = (uint8_t)kz;
-        }
-      }
-      h = fmaf(alpha, h, COMPL ? beta * x : x);
-      if (live) static_cast<IO*>(a.out)[at] = from_f32<IO>(h);
-    }
-    if (live && a.sT) a.sT[st] = h;
-    if (a.cu) {
-      if (s == 0) zero_rows<IO>(a, c, 0, lo);
-      if (s == nseq - 1) zero_rows<IO>(a, c, hi, a.T);
-    }
+// ------------------------------------------------- pairs (A, Bs) of 4 channels
+struct Pair {
+  float A[4], B[4];
+};
+__device__ __forceinline__ bool fresh(float A) { return __float_as_uint(A) == 0x80000000u; }
+// (A, B) of `a` followed by `b`.
+__device__ __forceinline__ void join(Pair& a, const Pair& b) {
+#pragma unroll
+  for (int j = 0; j < 4; ++j) {
+    const bool f = fresh(b.A[j]);
+    a.B[j] = f ? b.B[j] : fmaf(b.A[j], a.B[j], b.B[j]);
+    a.A[j] = f ? b.A[j] : a.A[j] * b.A[j];
   }
 }
+__device__ __forceinline__ void apply(float* c, const Pair& b) {
+#pragma unroll
+  for (int j = 0; j < 4; ++j) c[j] = fresh(b.A[j]) ? b.B[j] : fmaf(b.A[j], c[j], b.B[j]);
+}
+__device__ __forceinline__ void put_pair(float4* p, int lane, const Pair& q) {
+  p[lane] = make_float4(q.A[0], q.A[1], q.A[2], q.A[3]);
+  p[32 + lane] = make_float4(q.B[0], q.B[1], q.B[2], q.B[3]);
+}
+__device__ __forceinline__ void get_pair(const float4* p, int lane, Pair& q) {
+  const float4 a = p[lane], b = p[32 + lane];
+  q.A[0] = a.x, q.A[1] = a.y, q.A[2] = a.z, q.A[3] = a.w;
+  q.B[0] = b.x, q.B[1] = b.y, q.B[2] = b.z, q.B[3] = b.w;
+}
 
-template <typename IO, bool RAW, bool COMPL>
-__global__ void __launch_bounds__(kBlock) scan_bwd_kernel(const ScanArgs a) {
-  const int c = blockIdx.x * kBlock + threadIdx.x, nseq = a.cu ? a.N : a.B;
-  if (c >= a.D) return;
+// Words handed from block to block through L2: each is its own flag.
+__device__ __forceinline__ void publish4(float4* p, const float* v) {
+  uint32_t b[4];
+#pragma unroll
+  for (int j = 0; j < 4; ++j) b[j] = __float_as_uint(v[j]) == kEmpty ? 0x7fffffffu : __float_as_uint(v[j]);
+  asm volatile("st.relaxed.gpu.global.v4.b32 [%0], {%1, %2, %3, %4};" ::"l"(p), "r"(b[0]), "r"(b[1]), "r"(b[2]),
+               "r"(b[3])
+               : "memory");
+}
+__device__ __forceinline__ uint4 peek4(const float4* p) {
+  uint4 b;
+  asm volatile("ld.relaxed.gpu.global.v4.b32 {%0, %1, %2, %3}, [%4];"
+               : "=r"(b.x), "=r"(b.y), "=r"(b.z), "=r"(b.w)
+               : "l"(p)
+               : "memory");
+  return b;
+}
+__device__ __forceinline__ bool written(const uint4& b) {
+  return b.x != kEmpty && b.y != kEmpty && b.z != kEmpty && b.w != kEmpty;
+}
+
+// ------------------------------------------------------------------ the tiles
+enum Kind { kFwd, kFwdCkpt, kBwd, kBwdCkpt };
+
+// Input arrays of a stage, and rows per warp: a stage is 32 to 48 KiB (two
+// stages for each of two blocks per SM), 64 for the fp32 backward (one block).
+template <Kind K, typename IO, bool COMPL>
+struct Shape {
+  static constexpr bool kDown = K == kBwd || K == kBwdCkpt;
+  static constexpr int kIn = K == kBwd ? (COMPL ? 4 : 3) : K == kBwdCkpt ? 3 : 2;
+  static constexpr int kRows = sizeof(IO) == 4 || K == kBwd ? 4 : 8;  // per warp
+  static constexpr int kL = kWarps * kRows;
+  // element bytes of array i: forward x, g; backward dy, g, h, x; from the checkpoint dy, lambda, z
+  __host__ __device__ static constexpr int eb(int i) { return K == kBwdCkpt && i > 0 ? 1 : (int)sizeof(IO); }
+  __host__ __device__ static constexpr int at(int i) {
+    int o = 0;
+    for (int j = 0; j < i; ++j) o += kL * kBlock * eb(j);
+    return o;
+  }
+  static constexpr int kStage = at(kIn);
+  static constexpr int kSmem = kStages * kStage;
+  static constexpr int kPerSm = kSmem > 80 * 1024 ? 1 : 2;
+};
+
+struct TileArgs {
+  ScanArgs a;
+  CUtensorMap map[4];
+  WorkspaceHeader* hdr;     // error word; pad[0] is the ticket
+  float4* pairs;            // [chains][chunks][2][32]
+  float4* states;           // [chains][groups][32]
+  const int32_t* info;      // packed: sequence * 4 + first * 2 + last of each row, -1 outside
+  int chains, chunks, groups, blocks;  // blocks: of channels
+  bool tma, vec, in_order;
+};
+
+struct __align__(16) Shared {
+  float4 pair[2][kWarps][64];
+  float4 look[kWarps][64];
+  float4 carry[2][32];
+  uint64_t full[kStages], empty[kStages];
+  int tile[kStages];
+  int info[kStages][64];
+  uint8_t scale[kStages][2][64];
+};
+
+struct Row {
+  bool valid, first, last;
+  int seq;
+};
+
+template <Kind K, typename IO, bool RAW, bool COMPL>
+__global__ void __launch_bounds__(32 * (kWarps + 1), Shape<K, IO, COMPL>::kPerSm)
+    scan_tile_kernel(const __grid_constant__ TileArgs p) {
+  using S = Shape<K, IO, COMPL>;
+  constexpr int R = S::kRows, L = S::kL;
+  constexpr bool kDown = S::kDown, kSave = K == kFwdCkpt, kFrom = K == kBwdCkpt;
+  extern __shared__ __align__(128) uint8_t stages[];
+  __shared__ Shared sh;
+  const ScanArgs& a = p.a;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const size_t rows = (size_t)a.B * a.T;
-  const ScanCkptLayout l = scan_ckpt_layout(rows, a.D);
-  for (int s = blockIdx.y; s < nseq; s += gridDim.y) {
-    int64_t lo, hi;
-    rows_of(a, s, lo, hi);
-    const size_t st = (size_t)s * a.D + c;
-    float carry = a.s0 ? a.s0[st] : 0.f;
-    for (int64_t t = hi - 1; t >= lo; --t) {
-      const size_t at = (size_t)t * a.D + c;
-      float alpha, beta, z;
-      if (a.ckpt) {
-        gate<false>(decode(a.ckpt[t * l.pitch + c], pow2(a.ckpt[l.lam_scale + blockIdx.x * rows + t])), alpha, beta);
-        z = decode(a.ckpt[l.z + t * l.pitch + c], pow2(a.ckpt[l.z_scale + blockIdx.x * rows + t]));
+  const bool packed = a.cu != nullptr;
+
+  if (threadIdx.x == 0) {
+    for (int s = 0; s < kStages; ++s) mbar_init(&sh.full[s], 1), mbar_init(&sh.empty[s], kWarps);
+    fence_mbar_init();
+  }
+  __syncthreads();
+  grid_dep_wait();  // the workspace was prepared, and the inputs written, by earlier kernels
+
+  auto gave_up = [&](uint32_t where) {
+    atomicOr(&p.hdr->error, 1u);
+    atomicExch(&p.hdr->where, where);
+  };
+  auto first_row = [&](int chunk) { return (kDown ? p.chunks - 1 - chunk : chunk) * (int64_t)L; };
+
+  if (warp == kWarps) {
+    // ------------------------------------------------ producer: tickets, loads
+    uint32_t drawn = 0;
+    if (!p.in_order && lane == 0) drawn = atomicAdd(&p.hdr->pad[0], 1u);
+    for (int it = 0;; ++it) {
+      const int s = it % kStages;
+      int tile;
+      if (p.in_order) {
+        tile = it < p.chunks ? it * p.chains + (int)blockIdx.x : -1;
       } else {
-        gate<RAW>(load(static_cast<const IO*>(a.g), at), alpha, beta);
-        z = t > lo ? load(static_cast<const IO*>(a.h), at - a.D) : a.h0 ? a.h0[st] : 0.f;
-        if (COMPL) z -= load(static_cast<const IO*>(a.x), at);
+        const uint32_t t = __shfl_sync(0xffffffffu, drawn, 0);
+        tile = t < (uint32_t)p.chains * (uint32_t)p.chunks ? (int)t : -1;
+        if (tile >= 0 && lane == 0) drawn = atomicAdd(&p.hdr->pad[0], 1u);
       }
-      const float d = load(static_cast<const IO*>(a.dy), at) + carry;
-      carry = alpha * d;
-      static_cast<IO*>(a.out)[at] = from_f32<IO>(COMPL ? beta * d : d);
-      static_cast<IO*>(a.dg)[at] = from_f32<IO>(RAW ? carry * z * beta : carry * z);
+      if (it >= kStages && !mbar_wait(&sh.empty[s], (it / kStages - 1) & 1, kBarLimit) && lane == 0 && p.hdr)
+        gave_up(201);
+      if (lane == 0) sh.tile[s] = tile;
+      if (tile < 0) {
+        if (lane == 0) mbar_arrive(&sh.full[s]);
+        break;
+      }
+      const int chain = tile % p.chains, chunk = tile / p.chains, b = chain / p.blocks, cb = chain % p.blocks;
+      const int64_t t0 = first_row(chunk);
+      if (packed)
+        for (int i = lane; i < L; i += 32) sh.info[s][i] = t0 + i < a.T ? p.info[t0 + i] : -1;
+      if (kFrom) {
+        const ScanCkptLayout l = scan_ckpt_layout(rows, a.D);
+        for (int i = lane; i < L; i += 32) {
+          const size_t at = cb * rows + (size_t)b * a.T + t0 + i;
+          sh.scale[s][0][i] = t0 + i < a.T ? a.ckpt[l.lam_scale + at] : 1;
+          sh.scale[s][1][i] = t0 + i < a.T ? a.ckpt[l.z_scale + at] : 1;
+        }
+      }
+      __syncwarp();
+      if (lane == 0) {
+        if (p.tma) {
+          mbar_expect_tx(&sh.full[s], S::kStage);
+#pragma unroll
+          for (int i = 0; i < S::kIn; ++i)  // h one row up: what enters each row
+            tma_load_3d(stages + s * S::kStage + S::at(i), &p.map[i], &sh.full[s], cb * kBlock,
+                        (int)t0 - (K == kBwd && i == 2 ? 1 : 0), b);
+        } else {
+          mbar_arrive(&sh.full[s]);
+        }
+      }
     }
-    if (a.sT) a.sT[st] = carry;
-    if (a.cu) {
-      if (s == 0) zero_rows<IO>(a, c, 0, lo);
-      if (s == nseq - 1) zero_rows<IO>(a, c, hi, a.T);
+    return;
+  }
+
+  // ---------------------------------------------------------------- consumers
+  bool failed = false;
+  for (int it = 0;; ++it) {
+    const int s = it % kStages;
+    if (!mbar_wait(&sh.full[s], (it / kStages) & 1, kBarLimit) && p.hdr) gave_up(202);
+    const int tile = sh.tile[s];
+    if (tile < 0) break;
+    const int chain = tile % p.chains, chunk = tile / p.chains, b = chain / p.blocks, cb = chain % p.blocks;
+    const int64_t t0 = first_row(chunk);
+    const int c = cb * kBlock + lane * 4, n = a.D - c;  // this lane's channels, and how many there are (from 4 up: 4)
+    uint8_t* st = stages + s * S::kStage;
+    // row i of the tile that this warp handles r-th
+    auto row_at = [&](int r) { return kDown ? L - 1 - (warp * R + r) : warp * R + r; };
+    auto elem = [&](int arr, int i) { return st + S::at(arr) + (i * kBlock + lane * 4) * S::eb(arr); };
+    auto global_row = [&](int i) { return (size_t)b * a.T + t0 + i; };
+
+    if (!p.tma) {
+      // rows that TMA cannot take: each lane brings its own four channels
+      for (int r = 0; r < R; ++r) {
+        const int i = row_at(r);
+        const bool in = t0 + i < a.T;
+#pragma unroll
+        for (int arr = 0; arr < S::kIn; ++arr) {
+          if (kFrom && arr > 0) {
+            const ScanCkptLayout l = scan_ckpt_layout(rows, a.D);
+            uint32_t v = 0;
+            if (in && n > 0)
+              v = *reinterpret_cast<const uint32_t*>(a.ckpt + (arr == 2 ? l.z : 0) + global_row(i) * l.pitch + c);
+            *reinterpret_cast<uint32_t*>(elem(arr, i)) = v;
+            continue;
+          }
+          const void* src = K == kFwd || K == kFwdCkpt ? (arr == 0 ? a.x : a.g)
+                                                       : (arr == 0 ? a.dy : arr == 1 ? a.g : arr == 2 ? a.h : a.x);
+          const bool up = K == kBwd && arr == 2;
+          const bool ok = in && (!up || t0 + i > 0);
+          const IO* q = static_cast<const IO*>(src) + (ok ? (global_row(i) - up) * a.D + c : 0);
+          IO* d = reinterpret_cast<IO*>(elem(arr, i));
+#pragma unroll
+          for (int j = 0; j < 4; ++j) d[j] = ok && j < n ? q[j] : from_f32<IO>(0.f);
+        }
+      }
+      __syncwarp();
+    }
+
+    auto row_info = [&](int i) {
+      Row q;
+      if (packed) {
+        const int v = sh.info[s][i];
+        q.valid = v >= 0, q.first = v & 2, q.last = v & 1, q.seq = v >> 2;
+      } else {
+        const int64_t t = t0 + i;
+        q.valid = t < a.T, q.first = t == 0, q.last = t == a.T - 1, q.seq = b;
+      }
+      return q;
+    };
+    // whether any of the warp's rows starts or ends a sequence or belongs to none
+    bool edge = false;
+    if (lane < R) {
+      const Row q = row_info(row_at(lane));
+      edge = !q.valid || q.first || q.last;
+    }
+    edge = __any_sync(0xffffffffu, edge);
+    auto state_of = [&](const float* base, int seq, float* v) {
+      ldg4(base ? base + (size_t)seq * a.D + c : nullptr, v, n, p.vec);
+    };
+    auto gate_of = [&](int i, int j, const float* g, float& al, float& be) { gate<RAW && !kFrom>(g[j], al, be); };
+    auto load_gate = [&](int i, float* g) {
+      if constexpr (kFrom)
+        decode4(*reinterpret_cast<const uint32_t*>(elem(1, i)), pow2(sh.scale[s][0][i]), g);
+      else
+        lds4<IO>(elem(1, i), g);
+    };
+
+    // ---- the warp's rows as one pair
+    float al[R][4], u[R][4];  // alpha; forward: the input, backward: dL/dh
+    Pair mine;
+    auto reduce = [&](auto edges) {
+#pragma unroll
+      for (int j = 0; j < 4; ++j) mine.A[j] = 1.f, mine.B[j] = 0.f;
+#pragma unroll
+      for (int r = 0; r < R; ++r) {
+        const int i = row_at(r);
+        float g[4], v[4];
+        load_gate(i, g);
+        lds4<IO>(elem(0, i), v);
+        const Row q = edges.value ? row_info(i) : Row{true, false, false, 0};
+        float from[4];
+        const bool start = edges.value && q.valid && (kDown ? q.last : q.first);
+        if (start) state_of(a.s0, q.seq, from);
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+          float be;
+          gate_of(i, j, g, al[r][j], be);
+          u[r][j] = !kDown && COMPL ? be * v[j] : v[j];
+          if (edges.value && !q.valid) continue;
+          if (start) {
+            u[r][j] = kDown ? v[j] + from[j] : fmaf(al[r][j], from[j], u[r][j]);
+            mine.A[j] = -0.f;
+            mine.B[j] = kDown ? al[r][j] * u[r][j] : u[r][j];
+          } else {
+            mine.A[j] *= al[r][j];
+            mine.B[j] = kDown ? al[r][j] * (mine.B[j] + u[r][j]) : fmaf(al[r][j], mine.B[j], u[r][j]);
+          }
+        }
+      }
+    };
+    if (edge)
+      reduce(std::true_type{});
+    else
+      reduce(std::false_type{});
+
+    // ---- what enters the warp's rows
+    put_pair(sh.pair[it & 1][warp], lane, mine);
+    named_bar_sync(1, 32 * kWarps);
+    Pair before;  // of the tile's earlier warps
+#pragma unroll
+    for (int j = 0; j < 4; ++j) before.A[j] = 1.f, before.B[j] = 0.f;
+    for (int w = 0; w < warp; ++w) {
+      Pair q;
+      get_pair(sh.pair[it & 1][w], lane, q);
+      join(before, q);
+    }
+    float h[4] = {0.f, 0.f, 0.f, 0.f};  // the state that enters (forward), c_{t+1} (backward)
+    const int place = chunk % kGroup;
+    if (p.in_order) {
+      if (chunk > 0) {
+        const float4 q = sh.carry[it & 1][lane];
+        h[0] = q.x, h[1] = q.y, h[2] = q.z, h[3] = q.w;
+      }
+    } else {
+      float4* pairs = p.pairs + (size_t)chain * p.chunks * 64;
+      float4* states = p.states + (size_t)chain * p.groups * 32;
+      if (warp == kWarps - 1 && place != kGroup - 1 && chunk != p.chunks - 1) {
+        Pair all = before;
+        join(all, mine);
+        publish4(pairs + (size_t)chunk * 64 + lane, all.A);
+        publish4(pairs + (size_t)chunk * 64 + 32 + lane, all.B);
+      }
+      // the group's earlier tiles, shared out among the warps in order
+      const int lo = place * warp / kWarps, hi = place * (warp + 1) / kWarps;
+      const float4* head = states + (size_t)(chunk / kGroup - 1) * 32 + lane;
+      auto wait4 = [&](const float4* q, uint4 v) {
+        for (uint32_t i = 0; !__all_sync(0xffffffffu, written(v)); ++i) {
+          if (i >= (failed ? 1u : kPollLimit)) {
+            failed = true;
+            if (lane == 0) gave_up(203);
+            break;
+          }
+          v = peek4(q);
+        }
+        return make_float4(__uint_as_float(v.x), __uint_as_float(v.y), __uint_as_float(v.z), __uint_as_float(v.w));
+      };
+      uint4 hv = make_uint4(0, 0, 0, 0);
+      if (chunk >= kGroup) hv = peek4(head);
+      Pair part;
+#pragma unroll
+      for (int j = 0; j < 4; ++j) part.A[j] = 1.f, part.B[j] = 0.f;
+      for (int k = lo; k < hi; ++k) {
+        const float4* q = pairs + (size_t)(chunk - place + k) * 64 + lane;
+        const uint4 va = peek4(q), vb = peek4(q + 32);
+        const float4 A = wait4(q, va), B = wait4(q + 32, vb);
+        const Pair next{{A.x, A.y, A.z, A.w}, {B.x, B.y, B.z, B.w}};
+        join(part, next);
+      }
+      put_pair(sh.look[warp], lane, part);
+      named_bar_sync(1, 32 * kWarps);
+      if (chunk >= kGroup) {
+        const float4 q = wait4(head, hv);
+        h[0] = q.x, h[1] = q.y, h[2] = q.z, h[3] = q.w;
+      }
+      if (place)
+        for (int w = 0; w < kWarps; ++w) {
+          Pair q;
+          get_pair(sh.look[w], lane, q);
+          apply(h, q);
+        }
+    }
+    apply(h, before);
+
+    // ---- the rows themselves
+    int lam_code = 0, z_code = 0;  // of row `lane` of the warp
+    auto emit = [&](auto edges) {
+#pragma unroll
+      for (int r = 0; r < R; ++r) {
+        const int i = row_at(r);
+        const Row q = edges.value ? row_info(i) : Row{true, false, false, 0};
+        if (edges.value && !q.valid) {
+          if (packed && t0 + i < a.T) {  // a row that no sequence owns
+            const float zero[4] = {0.f, 0.f, 0.f, 0.f};
+            stg4(static_cast<IO*>(a.out) + global_row(i) * a.D + c, zero, n, p.vec);
+            if (kDown) stg4(static_cast<IO*>(a.dg) + global_row(i) * a.D + c, zero, n, p.vec);
+            if (kSave) {
+              const ScanCkptLayout l = scan_ckpt_layout(rows, a.D);
+              if (n > 0) {
+                *reinterpret_cast<uint32_t*>(a.ckpt + global_row(i) * l.pitch + c) = 0;
+                *reinterpret_cast<uint32_t*>(a.ckpt + l.z + global_row(i) * l.pitch + c) = 0;
+              }
+              if (lane == r) lam_code = z_code = 1;
+            }
+          }
+          continue;
+        }
+        const bool start = edges.value && (kDown ? q.last : q.first);
+        if constexpr (!kDown) {
+          float z[4], lam[4];
+          if constexpr (kSave) {
+            float g[4];
+            load_gate(i, g);
+            if (start)
+              state_of(a.s0, q.seq, z);
+            else
+#pragma unroll
+              for (int j = 0; j < 4; ++j) z[j] = h[j];
+            if (COMPL) {
+              float x[4];
+              lds4<IO>(elem(0, i), x);
+#pragma unroll
+              for (int j = 0; j < 4; ++j) z[j] -= x[j];
+            }
+#pragma unroll
+            for (int j = 0; j < 4; ++j) lam[j] = !RAW ? g[j] : j < n ? log_sigmoid(g[j]) : 0.f;
+          }
+#pragma unroll
+          for (int j = 0; j < 4; ++j) h[j] = start ? u[r][j] : fmaf(al[r][j], h[j], u[r][j]);
+          stg4(static_cast<IO*>(a.out) + global_row(i) * a.D + c, h, n, p.vec);
+          if constexpr (kSave) {
+            const ScanCkptLayout l = scan_ckpt_layout(rows, a.D);
+            uint32_t ml = 0, mz = 0;
+#pragma unroll
+            for (int j = 0; j < 4; ++j) ml = max(ml, magnitude(lam[j])), mz = max(mz, magnitude(z[j]));
+            const int kl = scale_code(__uint_as_float(__reduce_max_sync(0xffffffffu, ml)));
+            const int kz = scale_code(__uint_as_float(__reduce_max_sync(0xffffffffu, mz)));
+            if (n > 0) {
+              *reinterpret_cast<uint32_t*>(a.ckpt + global_row(i) * l.pitch + c) = encode4(lam, pow2(254 - kl));
+              *reinterpret_cast<uint32_t*>(a.ckpt + l.z + global_row(i) * l.pitch + c) = encode4(z, pow2(254 - kz));
+            }
+            if (lane == r) lam_code = kl, z_code = kz;
+          }
+          if (edges.value && q.last && a.sT) {
+#pragma unroll
+            for (int j = 0; j < 4; ++j)
+              if (j < n) a.sT[(size_t)q.seq * a.D + c + j] = h[j];
+          }
+        } else {
+          float z[4], g[4], dx[4], dg[4];
+          load_gate(i, g);
+          if constexpr (kFrom) {
+            decode4(*reinterpret_cast<const uint32_t*>(elem(2, i)), pow2(sh.scale[s][1][i]), z);
+          } else {
+            if (edges.value && q.first)
+              state_of(a.h0, q.seq, z);
+            else
+              lds4<IO>(elem(2, i), z);
+            if (COMPL) {
+              float x[4];
+              lds4<IO>(elem(3, i), x);
+#pragma unroll
+              for (int j = 0; j < 4; ++j) z[j] -= x[j];
+            }
+          }
+#pragma unroll
+          for (int j = 0; j < 4; ++j) {
+            float unused, be = 0.f;
+            if (COMPL || RAW) gate_of(i, j, g, unused, be);
+            const float d = start ? u[r][j] : u[r][j] + h[j];
+            h[j] = al[r][j] * d;
+            dx[j] = COMPL ? be * d : d;
+            dg[j] = RAW ? h[j] * z[j] * be : h[j] * z[j];
+          }
+          stg4(static_cast<IO*>(a.out) + global_row(i) * a.D + c, dx, n, p.vec);
+          stg4(static_cast<IO*>(a.dg) + global_row(i) * a.D + c, dg, n, p.vec);
+          if (edges.value && q.first && a.sT) {
+#pragma unroll
+            for (int j = 0; j < 4; ++j)
+              if (j < n) a.sT[(size_t)q.seq * a.D + c + j] = h[j];
+          }
+        }
+      }
+      if (kSave && lane < R && t0 + warp * R + lane < a.T) {
+        const ScanCkptLayout l = scan_ckpt_layout(rows, a.D);
+        const size_t at = cb * rows + global_row(warp * R + lane);
+        a.ckpt[l.lam_scale + at] = (uint8_t)lam_code;
+        a.ckpt[l.z_scale + at] = (uint8_t)z_code;
+      }
+    };
+    if (edge)
+      emit(std::true_type{});
+    else
+      emit(std::false_type{});
+
+    __syncwarp();
+    if (lane == 0) mbar_arrive(&sh.empty[s]);
+    if (warp == kWarps - 1) {  // the state that leaves the tile
+      if (p.in_order)
+        sh.carry[(it + 1) & 1][lane] = make_float4(h[0], h[1], h[2], h[3]);
+      else if (place == kGroup - 1)
+        publish4(p.states + ((size_t)chain * p.groups + chunk / kGroup) * 32 + lane, h);
     }
   }
 }
 
+// Before a sequence call: header and ticket cleared, the words that blocks
+// hand to each other marked as not written; packed: what each row is, and the
+// states of the empty sequences, whose final state is their initial state.
+__global__ void __launch_bounds__(256) scan_init_kernel(const TileArgs p, uint4* words, size_t count, int32_t* info) {
+  grid_dep_launch();
+  grid_dep_wait();
+  const size_t at = (size_t)blockIdx.x * 256 + threadIdx.x, step = (size_t)gridDim.x * 256;
+  if (at < sizeof(WorkspaceHeader) / 4) reinterpret_cast<uint32_t*>(p.hdr)[at] = 0;
+  for (size_t i = at; i < count; i += step) words[i] = make_uint4(kEmpty, kEmpty, kEmpty, kEmpty);
+  const ScanArgs& a = p.a;
+  if (!a.cu) return;
+  for (size_t t = at; t < (size_t)a.T; t += step) {
+    int lo = 0, hi = a.N + 1;  // the first of cu[0 .. N] that is past t
+    while (lo < hi) {
+      const int m = lo + (hi - lo) / 2;
+      if ((int64_t)__ldg(a.cu + m) <= (int64_t)t)
+        lo = m + 1;
+      else
+        hi = m;
+    }
+    int v = -1;
+    if (lo > 0 && lo <= a.N)
+      v = (lo - 1) * 4 + ((size_t)__ldg(a.cu + lo - 1) == t ? 2 : 0) + ((int64_t)__ldg(a.cu + lo) - 1 == (int64_t)t ? 1 : 0);
+    info[t] = v;
+  }
+  if (!a.sT || a.sT == a.s0) return;
+  for (int i = blockIdx.x; i < a.N; i += gridDim.x)
+    if (__ldg(a.cu + i + 1) <= __ldg(a.cu + i))
+      for (int c = threadIdx.x; c < a.D; c += 256) a.sT[(size_t)i * a.D + c] = a.s0 ? a.s0[(size_t)i * a.D + c] : 0.f;
+}
+
+// One token: a stream over state, x, g and h (14 B per element in bf16); four
+// channels per thread.
 template <typename IO, bool RAW, bool COMPL>
 __global__ void __launch_bounds__(256) scan_step_kernel(const IO* __restrict__ x, const IO* __restrict__ g,
                                                         const float* state, float* out_state, IO* __restrict__ h,
-                                                        size_t n) {
-  const size_t i = (size_t)blockIdx.x * 256 + threadIdx.x;
-  if (i >= n) return;
-  float alpha, beta;
-  gate<RAW>(to_f32(g[i]), alpha, beta);
-  const float v = to_f32(x[i]), r = fmaf(alpha, state[i], COMPL ? beta * v : v);
-  out_state[i] = r;
-  h[i] = from_f32<IO>(r);
+                                                        size_t count) {
+  const size_t i = ((size_t)blockIdx.x * 256 + threadIdx.x) * 4;
+  if (i >= count) return;
+  const int n = (int)min((size_t)4, count - i);
+  float gv[4], xv[4], s[4];
+  if (n == 4) {
+    lds4<IO>(reinterpret_cast<const uint8_t*>(g + i), gv);
+    lds4<IO>(reinterpret_cast<const uint8_t*>(x + i), xv);
+  } else {
+#pragma unroll
+    for (int j = 0; j < 4; ++j) gv[j] = j < n ? to_f32(g[i + j]) : 0.f, xv[j] = j < n ? to_f32(x[i + j]) : 0.f;
+  }
+  ldg4(state + i, s, n, n == 4);
+#pragma unroll
+  for (int j = 0; j < 4; ++j) {
+    float alpha, beta;
+    gate<RAW>(gv[j], alpha, beta);
+    s[j] = fmaf(alpha, s[j], COMPL ? beta * xv[j] : xv[j]);
+  }
+  stg4(out_state + i, s, n, n == 4);
+  stg4(h + i, s, n, n == 4);
 }
 
+// ========================================================================= host
 // Calls f with the flags as compile-time constants.
 template <typename F>
 cudaError_t with_flags(int dtype, int prep, int complement, F f) {
@@ -195,26 +688,146 @@ cudaError_t with_flags(int dtype, int prep, int complement, F f) {
   return dtype == KDA_F32 ? inner(float{}) : inner(__nv_bfloat16{});
 }
 
-dim3 scan_grid(const ScanArgs& a) {
-  const int nseq = a.cu ? a.N : a.B;
-  return dim3((unsigned)((a.D + kBlock - 1) / kBlock), (unsigned)(nseq < 65535 ? nseq : 65535));
+PFN_cuTensorMapEncodeTiled_v12000 encode_fn() {
+  static const PFN_cuTensorMapEncodeTiled_v12000 fn = [] {
+    void* p = nullptr;
+    cudaDriverEntryPointQueryResult q;
+    if (cudaGetDriverEntryPoint("cuTensorMapEncodeTiled", &p, cudaEnableDefault, &q) != cudaSuccess ||
+        q != cudaDriverEntryPointSuccess)
+      p = nullptr;
+    return reinterpret_cast<PFN_cuTensorMapEncodeTiled_v12000>(p);
+  }();
+  return fn;
+}
+
+// [B][T][row of `pitch` elements, `width` of them read]; box 128 channels x `box_rows` rows.
+bool make_map(CUtensorMap* map, const void* base, int eb, int B, int T, size_t width, size_t pitch, int box_rows) {
+  auto enc = encode_fn();
+  if (!enc) return false;
+  const CUtensorMapDataType type = eb == 4   ? CU_TENSOR_MAP_DATA_TYPE_FLOAT32
+                                   : eb == 2 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16
+                                             : CU_TENSOR_MAP_DATA_TYPE_UINT8;
+  cuuint64_t dims[3] = {width, (cuuint64_t)T, (cuuint64_t)B};
+  cuuint64_t strides[2] = {pitch * eb, pitch * eb * (cuuint64_t)T};
+  cuuint32_t box[3] = {(cuuint32_t)kBlock, (cuuint32_t)box_rows, 1}, es[3] = {1, 1, 1};
+  return enc(map, type, 3, const_cast<void*>(base), dims, strides, box, es, CU_TENSOR_MAP_INTERLEAVE_NONE,
+             CU_TENSOR_MAP_SWIZZLE_NONE, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+             CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+constexpr int kMinRows = kWarps * 4;  // of a tile, over all kinds
+
+int64_t div_up(int64_t a, int64_t b) { return (a + b - 1) / b; }
+size_t align256(size_t v) { return (v + 255) / 256 * 256; }
+
+int sm_count() {
+  int dev = 0, n = 0;
+  if (cudaGetDevice(&dev) != cudaSuccess || cudaDeviceGetAttribute(&n, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess)
+    return 148;
+  return n;
+}
+
+template <typename... P, typename... A>
+cudaError_t launch(void (*kernel)(P...), unsigned grid, unsigned threads, size_t smem, cudaStream_t stream, bool after,
+                   const A&... args) {
+  cudaLaunchConfig_t cfg{};
+  cfg.gridDim = dim3(grid), cfg.blockDim = dim3(threads), cfg.dynamicSmemBytes = smem, cfg.stream = stream;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = attr, cfg.numAttrs = after ? 1 : 0;
+  return cudaLaunchKernelEx(&cfg, kernel, args...);
+}
+
+template <Kind K, typename IO, bool RAW, bool COMPL>
+cudaError_t launch_tiles(const ScanArgs& a, void* ws, cudaStream_t stream) {
+  using S = Shape<K, IO, COMPL>;
+  TileArgs p;
+  p.a = a;
+  p.blocks = (int)div_up(a.D, kBlock);
+  const int64_t chains = (int64_t)a.B * p.blocks, chunks = div_up(a.T, S::kL);
+  p.chains = (int)chains, p.chunks = (int)chunks, p.groups = (int)div_up(chunks, kGroup);
+  p.in_order = a.T <= kInOrderRows;
+  p.vec = a.D % 4 == 0;
+  p.tma = (size_t)a.D * sizeof(IO) % 16 == 0;
+  // workspace: header, pairs, states, row information (the last two kinds of words only where needed)
+  uint8_t* w = static_cast<uint8_t*>(ws);
+  p.hdr = reinterpret_cast<WorkspaceHeader*>(w);
+  w += sizeof(WorkspaceHeader);
+  p.pairs = reinterpret_cast<float4*>(w);
+  const size_t pair_words = p.in_order ? 0 : (size_t)(chains * chunks) * 64;
+  const size_t state_words = p.in_order ? 0 : (size_t)chains * p.groups * 32;
+  p.states = p.pairs + pair_words;
+  int32_t* info = reinterpret_cast<int32_t*>(p.states + state_words);
+  p.info = info;
+  if (!ws || (p.in_order && !a.cu)) p.hdr = nullptr;  // no workspace
+  if (p.tma) {
+    const int eb = sizeof(IO);
+    const size_t d = (size_t)a.D;
+    bool ok;
+    if (K == kFwd || K == kFwdCkpt) {
+      ok = make_map(&p.map[0], a.x, eb, a.B, a.T, d, d, S::kL) && make_map(&p.map[1], a.g, eb, a.B, a.T, d, d, S::kL);
+    } else if (K == kBwd) {
+      ok = make_map(&p.map[0], a.dy, eb, a.B, a.T, d, d, S::kL) && make_map(&p.map[1], a.g, eb, a.B, a.T, d, d, S::kL) &&
+           make_map(&p.map[2], a.h, eb, a.B, a.T, d, d, S::kL) &&
+           (!COMPL || make_map(&p.map[3], a.x, eb, a.B, a.T, d, d, S::kL));
+    } else {
+      const ScanCkptLayout l = scan_ckpt_layout((size_t)a.B * a.T, a.D);
+      ok = make_map(&p.map[0], a.dy, eb, a.B, a.T, d, d, S::kL) &&
+           make_map(&p.map[1], a.ckpt, 1, a.B, a.T, d, l.pitch, S::kL) &&
+           make_map(&p.map[2], a.ckpt + l.z, 1, a.B, a.T, d, l.pitch, S::kL);
+    }
+    if (!ok) return cudaErrorInvalidValue;
+  }
+  auto kernel = scan_tile_kernel<K, IO, RAW, COMPL>;
+  static std::atomic<uint64_t> ready{0};  // devices whose shared-memory limit has been raised
+  int dev = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e != cudaSuccess) return e;
+  const uint64_t bit = dev < 64 ? uint64_t(1) << dev : 0;
+  if (!(ready.load(std::memory_order_relaxed) & bit) || !bit) {
+    e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, S::kSmem);
+    if (e != cudaSuccess) return e;
+    ready.fetch_or(bit, std::memory_order_relaxed);
+  }
+  const int sms = sm_count();
+  const bool init = !p.in_order || a.cu;
+  if (init) {
+    const size_t count = pair_words + state_words;
+    const int64_t blocks = std::min<int64_t>(std::max<int64_t>(div_up((int64_t)count, 256 * 4), div_up(a.cu ? a.T : 1, 256)), sms * 8);
+    e = launch(scan_init_kernel, (unsigned)std::max<int64_t>(blocks, 1), 256, 0, stream, false, p,
+               reinterpret_cast<uint4*>(p.pairs), count, info);
+    if (e != cudaSuccess) return e;
+  }
+  const int64_t grid = p.in_order ? chains : std::min<int64_t>(chains * chunks, (int64_t)sms * S::kPerSm);
+  return launch(kernel, (unsigned)grid, 32 * (kWarps + 1), S::kSmem, stream, init, p);
 }
 
 }  // namespace
 
-size_t scan_workspace_bytes(int, int, int, int, int) { return 0; }
+// Enough for every kind of call: the forward and the backward of a type share one size.
+size_t scan_workspace_bytes(int B, int T, int D, int N, int dtype) {
+  (void)dtype;
+  if (B == 0 || T == 0) return 0;
+  const int64_t chains = (int64_t)B * div_up(D, kBlock), chunks = div_up(T, kMinRows);
+  size_t bytes = 0;
+  if (T > kInOrderRows)
+    bytes = ((size_t)(chains * chunks) * 64 + (size_t)(chains * div_up(chunks, kGroup)) * 32) * sizeof(float4);
+  if (N > 0) bytes += align256((size_t)T * 4);
+  return bytes ? sizeof(WorkspaceHeader) + bytes : 0;
+}
 
-cudaError_t launch_scan_fwd(const ScanArgs& a, void*, cudaStream_t stream) {
+cudaError_t launch_scan_fwd(const ScanArgs& a, void* ws, cudaStream_t stream) {
   return with_flags(a.dtype, a.prep, a.complement, [&](auto io, auto raw, auto compl_) {
-    scan_fwd_kernel<decltype(io), raw.value, compl_.value><<<scan_grid(a), kBlock, 0, stream>>>(a);
-    return cudaGetLastError();
+    return a.ckpt ? launch_tiles<kFwdCkpt, decltype(io), raw.value, compl_.value>(a, ws, stream)
+                  : launch_tiles<kFwd, decltype(io), raw.value, compl_.value>(a, ws, stream);
   });
 }
 
-cudaError_t launch_scan_bwd(const ScanArgs& a, void*, cudaStream_t stream) {
+cudaError_t launch_scan_bwd(const ScanArgs& a, void* ws, cudaStream_t stream) {
   return with_flags(a.dtype, a.prep, a.complement, [&](auto io, auto raw, auto compl_) {
-    scan_bwd_kernel<decltype(io), raw.value, compl_.value><<<scan_grid(a), kBlock, 0, stream>>>(a);
-    return cudaGetLastError();
+    return a.ckpt ? launch_tiles<kBwdCkpt, decltype(io), raw.value, compl_.value>(a, ws, stream)
+                  : launch_tiles<kBwd, decltype(io), raw.value, compl_.value>(a, ws, stream);
   });
 }
 
@@ -222,7 +835,7 @@ cudaError_t launch_scan_step(const void* x, const void* g, const float* state, f
                              int dtype, int prep, int complement, cudaStream_t stream) {
   return with_flags(dtype, prep, complement, [&](auto io, auto raw, auto compl_) {
     using IO = decltype(io);
-    scan_step_kernel<IO, raw.value, compl_.value><<<(unsigned)((n + 255) / 256), 256, 0, stream>>>(
+    scan_step_kernel<IO, raw.value, compl_.value><<<(unsigned)((n + 1023) / 1024), 256, 0, stream>>>(
         static_cast<const IO*>(x), static_cast<const IO*>(g), state, out_state, static_cast<IO*>(h), n);
     return cudaGetLastError();
   });

@@ -363,7 +363,7 @@ KDA_API kda_status kda_recurrent_step_ex(const void* q, const void* k, const voi
  * cu_seqlens[i] <= t < cu_seqlens[i + 1] of the T rows, and the states are
  * [num_seqs, D].  Nothing passes from one sequence to another, not even an
  * infinity or NaN.  An empty sequence's final state is its initial state.
- * Rows outside every sequence are not read; they get zeros in h and the
+ * Rows outside every sequence are ignored; they get zeros in h and the
  * gradients.  The values must be non-decreasing and within [0, T]; they are
  * not checked (they live on the device): others give meaningless results, but
  * no access outside the buffers.  With cu_seqlens NULL, num_seqs is ignored.
@@ -400,7 +400,8 @@ KDA_API size_t kda_scan_checkpoint_size(int B, int T, int D);
 /*
  * The recurrence over T rows.
  *   initial_state : NULL for zeros
- *   final_state   : NULL to skip; may be initial_state's buffer
+ *   final_state   : NULL to skip; may be initial_state's buffer when no
+ *                   checkpoint is written
  *   checkpoint    : NULL, or kda_scan_checkpoint_size() bytes, 16-byte
  *                   aligned, written beside h
  *   workspace     : kda_scan_workspace_size() bytes, 256-byte aligned,
