@@ -18,17 +18,18 @@
 // the 8-bit checkpoint 8.  So the data is read once, in one pass: a tile is
 // 128 channels (one scale block of the checkpoint) x L rows; each of 8 warps
 // holds R = L / 8 rows x 128 channels of a tile as alpha and input in
-// registers, folds them to (A, Bs), and the 8 pairs are joined through shared
-// memory.  Tiles of one (sequence batch, channel block) chain are joined in
-// the order of the rows: each tile publishes its (A, Bs), the last of each
-// group of kGroup tiles the state that leaves the group; a tile folds the
-// pairs of its group's earlier tiles onto the state that left the group
-// before.  The order of the fold is fixed, so the bits are the same every
-// time.  Tiles are drawn by ticket in the order of the rows, so whatever a
-// tile waits for belongs to a block that is running; the words of the pairs
-// are their own flags (all bits set = not yet written), so one trip to L2
-// sees and fetches them.  A producer warp draws tickets and feeds the next
-// tiles by TMA while the current one is computed.
+// registers and folds them to (A, Bs).  Then one thread per channel folds the
+// 8 pairs and walks the state through them, so that each warp finds what
+// enters its rows and goes over them once more.  Tiles of one (batch, channel
+// block) chain are joined in the order of the rows: each tile publishes its
+// (A, Bs), the last of each group of kGroup tiles the state that leaves the
+// group; a tile folds the pairs of its group's earlier tiles onto the state
+// that left the group before.  The order of the fold is fixed, so the bits are
+// the same every time.  Tiles are drawn by ticket in the order of the rows, so
+// whatever a tile waits for belongs to a block that is running; the words of
+// the pairs are their own flags (all bits set = not yet written), so one trip
+// to L2 sees and fetches them.  While four warps do this, another draws the
+// next ticket and starts the tile after next on its way (TMA, three stages).
 #include <cudaTypedefs.h>
 #include <cuda_fp8.h>
 
@@ -44,26 +45,63 @@ namespace {
 
 using namespace sm100;
 constexpr int kBlock = 128;     // channels per tile and per scale of the checkpoint
-constexpr int kWarps = 8;       // consumer warps of a tile; one more feeds them
+constexpr int kWarps = 8;
+constexpr int kFeeder = 7;      // the warp that draws tickets and starts loads
 constexpr int kGroup = 16;      // tiles whose pairs are folded before a state is published
-constexpr int kStages = 2;
+constexpr int kStages = 3;
 constexpr int kInOrderRows = 256;  // chains of so few rows are walked by one block each
 constexpr uint32_t kEmpty = 0xffffffffu;     // a word not yet written
 constexpr uint32_t kPollLimit = 1u << 22;    // polls before a wait gives up
 constexpr uint32_t kBarLimit = 1u << 22;
 
-// alpha and 1 - alpha, each to a few ulp on its own (1 - alpha by subtraction
-// would lose the small rates that make the long memories), and, where asked
-// for, lambda.
+// exp(x) for x <= 126 ln 2, to about two ulp: 2^p for p = x / ln 2 rounded,
+// times 1 + (x - p ln 2), what the rounding left out.  x = -infinity gives NaN.
+__device__ __forceinline__ float exp_of(float x) {
+  const float p = x * 1.44269504f;
+  float e;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(e) : "f"(p));
+  return fmaf(e, fmaf(p, -0.693147181f, x), e);
+}
+__device__ __forceinline__ float rcp_of(float x) {
+  float r;
+  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
+  return r;
+}
+__device__ __forceinline__ float max_nan(float a, float b) {
+  float r;
+  asm("max.NaN.f32 %0, %1, %2;" : "=f"(r) : "f"(a), "f"(b));
+  return r;
+}
+__device__ __forceinline__ float min_nan(float a, float b) {
+  float r;
+  asm("min.NaN.f32 %0, %1, %2;" : "=f"(r) : "f"(a), "f"(b));
+  return r;
+}
+// 1 - exp(x) for x <= 0 given alpha = exp(x): the series where the difference
+// would lose the small rates that make the long memories.
+__device__ __forceinline__ float rate_of(float x, float alpha) {
+  float q = fmaf(x, 1.f / 40320.f, 1.f / 5040.f);
+  q = fmaf(x, q, 1.f / 720.f);
+  q = fmaf(x, q, 1.f / 120.f);
+  q = fmaf(x, q, 1.f / 24.f);
+  q = fmaf(x, q, 1.f / 6.f);
+  q = fmaf(x, q, 0.5f);
+  q = fmaf(x, q, 1.f);
+  return fabsf(x) < 0.5f ? -x * q : 1.f - alpha;
+}
+// alpha and 1 - alpha of a gate, each to a few ulp on its own.  The clamps
+// keep the exponent's residual a number; past them exp is below 2^-126 and
+// counts as zero.  NaN stays NaN.
 template <bool RAW>
 __device__ __forceinline__ void gate(float g, float& alpha, float& beta) {
   if (RAW) {
-    const float e = expf(-fabsf(g)), inv = __frcp_rn(1.f + e), lo = e * inv;
-    alpha = g >= 0.f ? inv : lo;
-    beta = g >= 0.f ? lo : inv;
+    const float e = exp_of(-min_nan(fabsf(g), 128.f)), hi = rcp_of(1.f + e), lo = e * hi;
+    alpha = g >= 0.f ? hi : lo;
+    beta = g >= 0.f ? lo : hi;
   } else {
-    alpha = expf(g);
-    beta = -expm1f(g);
+    const float x = max_nan(g, -128.f);
+    alpha = exp_of(x);
+    beta = rate_of(x, alpha);
   }
 }
 
@@ -141,60 +179,27 @@ __device__ __forceinline__ void ldg4(const float* p, float* v, int n, bool vec) 
   }
 }
 
-// ------------------------------------------------- pairs (A, Bs) of 4 channels
-struct Pair {
-  float A[4], B[4];
-};
+// ------------------------------------------------------------- pairs (A, Bs)
 __device__ __forceinline__ bool fresh(float A) { return __float_as_uint(A) == 0x80000000u; }
-// (A, B) of `a` followed by `b`.
-__device__ __forceinline__ void join(Pair& a, const Pair& b) {
-#pragma unroll
-  for (int j = 0; j < 4; ++j) {
-    const bool f = fresh(b.A[j]);
-    a.B[j] = f ? b.B[j] : fmaf(b.A[j], a.B[j], b.B[j]);
-    a.A[j] = f ? b.A[j] : a.A[j] * b.A[j];
-  }
-}
-__device__ __forceinline__ void apply(float* c, const Pair& b) {
-#pragma unroll
-  for (int j = 0; j < 4; ++j) c[j] = fresh(b.A[j]) ? b.B[j] : fmaf(b.A[j], c[j], b.B[j]);
-}
-__device__ __forceinline__ void put_pair(float4* p, int lane, const Pair& q) {
-  p[lane] = make_float4(q.A[0], q.A[1], q.A[2], q.A[3]);
-  p[32 + lane] = make_float4(q.B[0], q.B[1], q.B[2], q.B[3]);
-}
-__device__ __forceinline__ void get_pair(const float4* p, int lane, Pair& q) {
-  const float4 a = p[lane], b = p[32 + lane];
-  q.A[0] = a.x, q.A[1] = a.y, q.A[2] = a.z, q.A[3] = a.w;
-  q.B[0] = b.x, q.B[1] = b.y, q.B[2] = b.z, q.B[3] = b.w;
-}
+// What leaves a stretch (A, B) that c enters.
+__device__ __forceinline__ float through(float c, float A, float B) { return fresh(A) ? B : fmaf(A, c, B); }
 
 // Words handed from block to block through L2: each is its own flag.
-__device__ __forceinline__ void publish4(float4* p, const float* v) {
-  uint32_t b[4];
-#pragma unroll
-  for (int j = 0; j < 4; ++j) b[j] = __float_as_uint(v[j]) == kEmpty ? 0x7fffffffu : __float_as_uint(v[j]);
-  asm volatile("st.relaxed.gpu.global.v4.b32 [%0], {%1, %2, %3, %4};" ::"l"(p), "r"(b[0]), "r"(b[1]), "r"(b[2]),
-               "r"(b[3])
-               : "memory");
+__device__ __forceinline__ void publish(float* p, float v) {
+  const uint32_t b = __float_as_uint(v) == kEmpty ? 0x7fffffffu : __float_as_uint(v);
+  asm volatile("st.relaxed.gpu.global.b32 [%0], %1;" ::"l"(p), "r"(b) : "memory");
 }
-__device__ __forceinline__ uint4 peek4(const float4* p) {
-  uint4 b;
-  asm volatile("ld.relaxed.gpu.global.v4.b32 {%0, %1, %2, %3}, [%4];"
-               : "=r"(b.x), "=r"(b.y), "=r"(b.z), "=r"(b.w)
-               : "l"(p)
-               : "memory");
+__device__ __forceinline__ uint32_t peek(const float* p) {
+  uint32_t b;
+  asm volatile("ld.relaxed.gpu.global.b32 %0, [%1];" : "=r"(b) : "l"(p) : "memory");
   return b;
-}
-__device__ __forceinline__ bool written(const uint4& b) {
-  return b.x != kEmpty && b.y != kEmpty && b.z != kEmpty && b.w != kEmpty;
 }
 
 // ------------------------------------------------------------------ the tiles
 enum Kind { kFwd, kFwdCkpt, kBwd, kBwdCkpt };
 
-// Input arrays of a stage, and rows per warp: a stage is 32 to 48 KiB (two
-// stages for each of two blocks per SM), 64 for the fp32 backward (one block).
+// Input arrays of a stage, and rows per warp: a stage is 24 or 32 KiB, three
+// of them and two blocks per SM (the fp32 backward: 48 or 64 KiB, one block).
 template <Kind K, typename IO, bool COMPL>
 struct Shape {
   static constexpr bool kDown = K == kBwd || K == kBwdCkpt;
@@ -210,25 +215,25 @@ struct Shape {
   }
   static constexpr int kStage = at(kIn);
   static constexpr int kSmem = kStages * kStage;
-  static constexpr int kPerSm = kSmem > 80 * 1024 ? 1 : 2;
+  static constexpr int kPerSm = kSmem > 96 * 1024 ? 1 : 2;
 };
 
 struct TileArgs {
   ScanArgs a;
   CUtensorMap map[4];
   WorkspaceHeader* hdr;     // error word; pad[0] is the ticket
-  float4* pairs;            // [chains][chunks][2][32]
-  float4* states;           // [chains][groups][32]
+  float* pairs;             // [chains][chunks][2][128]
+  float* states;            // [chains][groups][128]
   const int32_t* info;      // packed: sequence * 4 + first * 2 + last of each row, -1 outside
   int chains, chunks, groups, blocks;  // blocks: of channels
   bool tma, vec, in_order;
 };
 
 struct __align__(16) Shared {
-  float4 pair[2][kWarps][64];
-  float4 look[kWarps][64];
-  float4 carry[2][32];
-  uint64_t full[kStages], empty[kStages];
+  float pair[kWarps][2][kBlock];  // (A, Bs) of each warp's rows
+  float enter[kWarps][kBlock];    // what enters them
+  float carry[kBlock];            // in order: what leaves the tile
+  uint64_t full[kStages];
   int tile[kStages];
   int info[kStages][64];
   uint8_t scale[kStages][2][64];
@@ -240,7 +245,7 @@ struct Row {
 };
 
 template <Kind K, typename IO, bool RAW, bool COMPL>
-__global__ void __launch_bounds__(32 * (kWarps + 1), Shape<K, IO, COMPL>::kPerSm)
+__global__ void __launch_bounds__(32 * kWarps, Shape<K, IO, COMPL>::kPerSm)
     scan_tile_kernel(const __grid_constant__ TileArgs p) {
   using S = Shape<K, IO, COMPL>;
   constexpr int R = S::kRows, L = S::kL;
@@ -253,73 +258,71 @@ __global__ void __launch_bounds__(32 * (kWarps + 1), Shape<K, IO, COMPL>::kPerSm
   const bool packed = a.cu != nullptr;
 
   if (threadIdx.x == 0) {
-    for (int s = 0; s < kStages; ++s) mbar_init(&sh.full[s], 1), mbar_init(&sh.empty[s], kWarps);
+    for (int s = 0; s < kStages; ++s) mbar_init(&sh.full[s], 2);
     fence_mbar_init();
   }
   __syncthreads();
   grid_dep_wait();  // the workspace was prepared, and the inputs written, by earlier kernels
 
   auto gave_up = [&](uint32_t where) {
+    if (!p.hdr) return;
     atomicOr(&p.hdr->error, 1u);
     atomicExch(&p.hdr->where, where);
   };
   auto first_row = [&](int chunk) { return (kDown ? p.chunks - 1 - chunk : chunk) * (int64_t)L; };
 
-  if (warp == kWarps) {
-    // ------------------------------------------------ producer: tickets, loads
-    uint32_t drawn = 0;
-    if (!p.in_order && lane == 0) drawn = atomicAdd(&p.hdr->pad[0], 1u);
-    for (int it = 0;; ++it) {
-      const int s = it % kStages;
-      int tile;
-      if (p.in_order) {
-        tile = it < p.chunks ? it * p.chains + (int)blockIdx.x : -1;
-      } else {
-        const uint32_t t = __shfl_sync(0xffffffffu, drawn, 0);
-        tile = t < (uint32_t)p.chains * (uint32_t)p.chunks ? (int)t : -1;
-        if (tile >= 0 && lane == 0) drawn = atomicAdd(&p.hdr->pad[0], 1u);
-      }
-      if (it >= kStages && !mbar_wait(&sh.empty[s], (it / kStages - 1) & 1, kBarLimit) && lane == 0 && p.hdr)
-        gave_up(201);
-      if (lane == 0) sh.tile[s] = tile;
-      if (tile < 0) {
-        if (lane == 0) mbar_arrive(&sh.full[s]);
-        break;
-      }
-      const int chain = tile % p.chains, chunk = tile / p.chains, b = chain / p.blocks, cb = chain % p.blocks;
-      const int64_t t0 = first_row(chunk);
-      if (packed)
-        for (int i = lane; i < L; i += 32) sh.info[s][i] = t0 + i < a.T ? p.info[t0 + i] : -1;
-      if (kFrom) {
-        const ScanCkptLayout l = scan_ckpt_layout(rows, a.D);
-        for (int i = lane; i < L; i += 32) {
-          const size_t at = cb * rows + (size_t)b * a.T + t0 + i;
-          sh.scale[s][0][i] = t0 + i < a.T ? a.ckpt[l.lam_scale + at] : 1;
-          sh.scale[s][1][i] = t0 + i < a.T ? a.ckpt[l.z_scale + at] : 1;
-        }
-      }
-      __syncwarp();
-      if (lane == 0) {
-        if (p.tma) {
-          mbar_expect_tx(&sh.full[s], S::kStage);
+  // ---- the feeder: tile `it` of this block into its stage
+  uint32_t drawn = 0;  // lane 0: the next ticket
+  if (warp == kFeeder && lane == 0 && !p.in_order) drawn = atomicAdd(&p.hdr->pad[0], 1u);
+  bool fed_all = false;
+  auto feed = [&](int it) {
+    if (fed_all) return;
+    const int s = it % kStages;
+    int tile;
+    if (p.in_order) {
+      tile = it < p.chunks ? it * p.chains + (int)blockIdx.x : -1;
+    } else {
+      const uint32_t t = __shfl_sync(0xffffffffu, drawn, 0);
+      tile = t < (uint32_t)p.chains * (uint32_t)p.chunks ? (int)t : -1;
+      if (tile >= 0 && lane == 0) drawn = atomicAdd(&p.hdr->pad[0], 1u);
+    }
+    if (lane == 0) sh.tile[s] = tile;
+    if (tile < 0) {
+      if (lane == 0) mbar_arrive(&sh.full[s]), mbar_arrive(&sh.full[s]);
+      fed_all = true;
+      return;
+    }
+    const int chain = tile % p.chains, chunk = tile / p.chains, b = chain / p.blocks, cb = chain % p.blocks;
+    const int64_t t0 = first_row(chunk);
+    if (lane == 0 && p.tma) {
+      mbar_expect_tx(&sh.full[s], S::kStage);
 #pragma unroll
-          for (int i = 0; i < S::kIn; ++i)  // h one row up: what enters each row
-            tma_load_3d(stages + s * S::kStage + S::at(i), &p.map[i], &sh.full[s], cb * kBlock,
-                        (int)t0 - (K == kBwd && i == 2 ? 1 : 0), b);
-        } else {
-          mbar_arrive(&sh.full[s]);
-        }
+      for (int i = 0; i < S::kIn; ++i)  // h one row up: what enters each row
+        tma_load_3d(stages + s * S::kStage + S::at(i), &p.map[i], &sh.full[s], cb * kBlock,
+                    (int)t0 - (K == kBwd && i == 2 ? 1 : 0), b);
+    }
+    if (packed)
+      for (int i = lane; i < L; i += 32) sh.info[s][i] = t0 + i < a.T ? p.info[t0 + i] : -1;
+    if (kFrom) {
+      const ScanCkptLayout l = scan_ckpt_layout(rows, a.D);
+      for (int i = lane; i < L; i += 32) {
+        const size_t at = cb * rows + (size_t)b * a.T + t0 + i;
+        sh.scale[s][0][i] = t0 + i < a.T ? a.ckpt[l.lam_scale + at] : 1;
+        sh.scale[s][1][i] = t0 + i < a.T ? a.ckpt[l.z_scale + at] : 1;
       }
     }
-    return;
-  }
+    __syncwarp();
+    if (lane == 0) mbar_arrive(&sh.full[s]);
+    if (lane == 0 && !p.tma) mbar_arrive(&sh.full[s]);
+  };
+  if (warp == kFeeder) feed(0), feed(1);
 
-  // ---------------------------------------------------------------- consumers
   bool failed = false;
   for (int it = 0;; ++it) {
     const int s = it % kStages;
-    if (!mbar_wait(&sh.full[s], (it / kStages) & 1, kBarLimit) && p.hdr) gave_up(202);
-    const int tile = sh.tile[s];
+    const bool there = mbar_wait(&sh.full[s], (it / kStages) & 1, kBarLimit);
+    if (!there) gave_up(202);
+    const int tile = there ? sh.tile[s] : -1;
     if (tile < 0) break;
     const int chain = tile % p.chains, chunk = tile / p.chains, b = chain / p.blocks, cb = chain % p.blocks;
     const int64_t t0 = first_row(chunk);
@@ -379,7 +382,6 @@ __global__ void __launch_bounds__(32 * (kWarps + 1), Shape<K, IO, COMPL>::kPerSm
     auto state_of = [&](const float* base, int seq, float* v) {
       ldg4(base ? base + (size_t)seq * a.D + c : nullptr, v, n, p.vec);
     };
-    auto gate_of = [&](int i, int j, const float* g, float& al, float& be) { gate<RAW && !kFrom>(g[j], al, be); };
     auto load_gate = [&](int i, float* g) {
       if constexpr (kFrom)
         decode4(*reinterpret_cast<const uint32_t*>(elem(1, i)), pow2(sh.scale[s][0][i]), g);
@@ -388,11 +390,11 @@ __global__ void __launch_bounds__(32 * (kWarps + 1), Shape<K, IO, COMPL>::kPerSm
     };
 
     // ---- the warp's rows as one pair
-    float al[R][4], u[R][4];  // alpha; forward: the input, backward: dL/dh
-    Pair mine;
+    float al[R][4], u[R][4];  // alpha; forward: the input, backward: 1 - alpha
+    float A[4], B[4];
     auto reduce = [&](auto edges) {
 #pragma unroll
-      for (int j = 0; j < 4; ++j) mine.A[j] = 1.f, mine.B[j] = 0.f;
+      for (int j = 0; j < 4; ++j) A[j] = 1.f, B[j] = 0.f;
 #pragma unroll
       for (int r = 0; r < R; ++r) {
         const int i = row_at(r);
@@ -406,16 +408,16 @@ __global__ void __launch_bounds__(32 * (kWarps + 1), Shape<K, IO, COMPL>::kPerSm
 #pragma unroll
         for (int j = 0; j < 4; ++j) {
           float be;
-          gate_of(i, j, g, al[r][j], be);
-          u[r][j] = !kDown && COMPL ? be * v[j] : v[j];
+          gate<RAW && !kFrom>(g[j], al[r][j], be);
+          u[r][j] = kDown ? be : COMPL ? be * v[j] : v[j];
           if (edges.value && !q.valid) continue;
           if (start) {
-            u[r][j] = kDown ? v[j] + from[j] : fmaf(al[r][j], from[j], u[r][j]);
-            mine.A[j] = -0.f;
-            mine.B[j] = kDown ? al[r][j] * u[r][j] : u[r][j];
+            if (!kDown) u[r][j] = fmaf(al[r][j], from[j], u[r][j]);
+            A[j] = -0.f;
+            B[j] = kDown ? al[r][j] * (v[j] + from[j]) : u[r][j];
           } else {
-            mine.A[j] *= al[r][j];
-            mine.B[j] = kDown ? al[r][j] * (mine.B[j] + u[r][j]) : fmaf(al[r][j], mine.B[j], u[r][j]);
+            A[j] *= al[r][j];
+            B[j] = kDown ? al[r][j] * (B[j] + v[j]) : fmaf(al[r][j], B[j], u[r][j]);
           }
         }
       }
@@ -424,74 +426,74 @@ __global__ void __launch_bounds__(32 * (kWarps + 1), Shape<K, IO, COMPL>::kPerSm
       reduce(std::true_type{});
     else
       reduce(std::false_type{});
+    *reinterpret_cast<float4*>(&sh.pair[warp][0][lane * 4]) = make_float4(A[0], A[1], A[2], A[3]);
+    *reinterpret_cast<float4*>(&sh.pair[warp][1][lane * 4]) = make_float4(B[0], B[1], B[2], B[3]);
+    __syncthreads();  // the pairs are there, and every warp is done with the tile before
 
-    // ---- what enters the warp's rows
-    put_pair(sh.pair[it & 1][warp], lane, mine);
-    named_bar_sync(1, 32 * kWarps);
-    Pair before;  // of the tile's earlier warps
-#pragma unroll
-    for (int j = 0; j < 4; ++j) before.A[j] = 1.f, before.B[j] = 0.f;
-    for (int w = 0; w < warp; ++w) {
-      Pair q;
-      get_pair(sh.pair[it & 1][w], lane, q);
-      join(before, q);
-    }
-    float h[4] = {0.f, 0.f, 0.f, 0.f};  // the state that enters (forward), c_{t+1} (backward)
+    // ---- what enters each warp's rows: one thread per channel
     const int place = chunk % kGroup;
-    if (p.in_order) {
-      if (chunk > 0) {
-        const float4 q = sh.carry[it & 1][lane];
-        h[0] = q.x, h[1] = q.y, h[2] = q.z, h[3] = q.w;
-      }
-    } else {
-      float4* pairs = p.pairs + (size_t)chain * p.chunks * 64;
-      float4* states = p.states + (size_t)chain * p.groups * 32;
-      if (warp == kWarps - 1 && place != kGroup - 1 && chunk != p.chunks - 1) {
-        Pair all = before;
-        join(all, mine);
-        publish4(pairs + (size_t)chunk * 64 + lane, all.A);
-        publish4(pairs + (size_t)chunk * 64 + 32 + lane, all.B);
-      }
-      // the group's earlier tiles, shared out among the warps in order
-      const int lo = place * warp / kWarps, hi = place * (warp + 1) / kWarps;
-      const float4* head = states + (size_t)(chunk / kGroup - 1) * 32 + lane;
-      auto wait4 = [&](const float4* q, uint4 v) {
-        for (uint32_t i = 0; !__all_sync(0xffffffffu, written(v)); ++i) {
-          if (i >= (failed ? 1u : kPollLimit)) {
-            failed = true;
-            if (lane == 0) gave_up(203);
-            break;
-          }
-          v = peek4(q);
-        }
-        return make_float4(__uint_as_float(v.x), __uint_as_float(v.y), __uint_as_float(v.z), __uint_as_float(v.w));
-      };
-      uint4 hv = make_uint4(0, 0, 0, 0);
-      if (chunk >= kGroup) hv = peek4(head);
-      Pair part;
+    if (warp < kBlock / 32) {
+      const int ch = threadIdx.x;
+      float* pairs = p.pairs + ((size_t)chain * p.chunks + chunk) * (2 * kBlock) + ch;
+      if (!p.in_order && place != kGroup - 1 && chunk != p.chunks - 1) {
+        float ta = sh.pair[0][0][ch], tb = sh.pair[0][1][ch];
 #pragma unroll
-      for (int j = 0; j < 4; ++j) part.A[j] = 1.f, part.B[j] = 0.f;
-      for (int k = lo; k < hi; ++k) {
-        const float4* q = pairs + (size_t)(chunk - place + k) * 64 + lane;
-        const uint4 va = peek4(q), vb = peek4(q + 32);
-        const float4 A = wait4(q, va), B = wait4(q + 32, vb);
-        const Pair next{{A.x, A.y, A.z, A.w}, {B.x, B.y, B.z, B.w}};
-        join(part, next);
-      }
-      put_pair(sh.look[warp], lane, part);
-      named_bar_sync(1, 32 * kWarps);
-      if (chunk >= kGroup) {
-        const float4 q = wait4(head, hv);
-        h[0] = q.x, h[1] = q.y, h[2] = q.z, h[3] = q.w;
-      }
-      if (place)
-        for (int w = 0; w < kWarps; ++w) {
-          Pair q;
-          get_pair(sh.look[w], lane, q);
-          apply(h, q);
+        for (int w = 1; w < kWarps; ++w) {
+          const float wa = sh.pair[w][0][ch], wb = sh.pair[w][1][ch];
+          tb = through(tb, wa, wb);
+          ta = fresh(wa) ? wa : ta * wa;
         }
+        publish(pairs, ta);
+        publish(pairs + kBlock, tb);
+      }
+      float h = 0.f;
+      if (p.in_order) {
+        if (chunk > 0) h = sh.carry[ch];
+      } else {
+        auto arrived = [&](const float* q, uint32_t v) {
+          for (uint32_t i = 0; v == kEmpty; ++i) {
+            if (i >= (failed ? 1u : kPollLimit)) {
+              failed = true;
+              gave_up(203);
+              break;
+            }
+            v = peek(q);
+          }
+          return __uint_as_float(v);
+        };
+        const float* head = p.states + ((size_t)chain * p.groups + chunk / kGroup - 1) * kBlock + ch;
+        uint32_t hv = 0, va[kGroup - 1], vb[kGroup - 1];
+        if (chunk >= kGroup) hv = peek(head);
+        const float* q = pairs - (size_t)place * (2 * kBlock);
+#pragma unroll
+        for (int k = 0; k < kGroup - 1; ++k)
+          if (k < place) va[k] = peek(q + k * 2 * kBlock), vb[k] = peek(q + (k * 2 + 1) * kBlock);
+        if (chunk >= kGroup) h = arrived(head, hv);
+#pragma unroll
+        for (int k = 0; k < kGroup - 1; ++k)
+          if (k < place) {
+            const float ka = arrived(q + k * 2 * kBlock, va[k]), kb = arrived(q + (k * 2 + 1) * kBlock, vb[k]);
+            h = through(h, ka, kb);
+          }
+      }
+#pragma unroll
+      for (int w = 0; w < kWarps; ++w) {
+        sh.enter[w][ch] = h;
+        h = through(h, sh.pair[w][0][ch], sh.pair[w][1][ch]);
+      }
+      if (p.in_order)
+        sh.carry[ch] = h;
+      else if (place == kGroup - 1)
+        publish(p.states + ((size_t)chain * p.groups + chunk / kGroup) * kBlock + ch, h);
+    } else if (warp == kFeeder) {
+      feed(it + 2);  // into the stage of the tile before this one
     }
-    apply(h, before);
+    __syncthreads();
+    float h[4];  // the state that enters (forward), c_{t+1} (backward)
+    {
+      const float4 q = *reinterpret_cast<const float4*>(&sh.enter[warp][lane * 4]);
+      h[0] = q.x, h[1] = q.y, h[2] = q.z, h[3] = q.w;
+    }
 
     // ---- the rows themselves
     int lam_code = 0, z_code = 0;  // of row `lane` of the warp
@@ -558,8 +560,9 @@ __global__ void __launch_bounds__(32 * (kWarps + 1), Shape<K, IO, COMPL>::kPerSm
               if (j < n) a.sT[(size_t)q.seq * a.D + c + j] = h[j];
           }
         } else {
-          float z[4], g[4], dx[4], dg[4];
-          load_gate(i, g);
+          float z[4], v[4], dx[4], dg[4], from[4];
+          lds4<IO>(elem(0, i), v);
+          if (start) state_of(a.s0, q.seq, from);
           if constexpr (kFrom) {
             decode4(*reinterpret_cast<const uint32_t*>(elem(2, i)), pow2(sh.scale[s][1][i]), z);
           } else {
@@ -576,12 +579,10 @@ __global__ void __launch_bounds__(32 * (kWarps + 1), Shape<K, IO, COMPL>::kPerSm
           }
 #pragma unroll
           for (int j = 0; j < 4; ++j) {
-            float unused, be = 0.f;
-            if (COMPL || RAW) gate_of(i, j, g, unused, be);
-            const float d = start ? u[r][j] : u[r][j] + h[j];
+            const float d = v[j] + (start ? from[j] : h[j]);
             h[j] = al[r][j] * d;
-            dx[j] = COMPL ? be * d : d;
-            dg[j] = RAW ? h[j] * z[j] * be : h[j] * z[j];
+            dx[j] = COMPL ? u[r][j] * d : d;
+            dg[j] = RAW ? h[j] * z[j] * u[r][j] : h[j] * z[j];
           }
           stg4(static_cast<IO*>(a.out) + global_row(i) * a.D + c, dx, n, p.vec);
           stg4(static_cast<IO*>(a.dg) + global_row(i) * a.D + c, dg, n, p.vec);
@@ -603,15 +604,6 @@ __global__ void __launch_bounds__(32 * (kWarps + 1), Shape<K, IO, COMPL>::kPerSm
       emit(std::true_type{});
     else
       emit(std::false_type{});
-
-    __syncwarp();
-    if (lane == 0) mbar_arrive(&sh.empty[s]);
-    if (warp == kWarps - 1) {  // the state that leaves the tile
-      if (p.in_order)
-        sh.carry[(it + 1) & 1][lane] = make_float4(h[0], h[1], h[2], h[3]);
-      else if (place == kGroup - 1)
-        publish4(p.states + ((size_t)chain * p.groups + chunk / kGroup) * 32 + lane, h);
-    }
   }
 }
 
@@ -754,9 +746,9 @@ cudaError_t launch_tiles(const ScanArgs& a, void* ws, cudaStream_t stream) {
   uint8_t* w = static_cast<uint8_t*>(ws);
   p.hdr = reinterpret_cast<WorkspaceHeader*>(w);
   w += sizeof(WorkspaceHeader);
-  p.pairs = reinterpret_cast<float4*>(w);
-  const size_t pair_words = p.in_order ? 0 : (size_t)(chains * chunks) * 64;
-  const size_t state_words = p.in_order ? 0 : (size_t)chains * p.groups * 32;
+  p.pairs = reinterpret_cast<float*>(w);
+  const size_t pair_words = p.in_order ? 0 : (size_t)(chains * chunks) * (2 * kBlock);
+  const size_t state_words = p.in_order ? 0 : (size_t)chains * p.groups * kBlock;
   p.states = p.pairs + pair_words;
   int32_t* info = reinterpret_cast<int32_t*>(p.states + state_words);
   p.info = info;
@@ -793,14 +785,14 @@ cudaError_t launch_tiles(const ScanArgs& a, void* ws, cudaStream_t stream) {
   const int sms = sm_count();
   const bool init = !p.in_order || a.cu;
   if (init) {
-    const size_t count = pair_words + state_words;
+    const size_t count = (pair_words + state_words) / 4;
     const int64_t blocks = std::min<int64_t>(std::max<int64_t>(div_up((int64_t)count, 256 * 4), div_up(a.cu ? a.T : 1, 256)), sms * 8);
     e = launch(scan_init_kernel, (unsigned)std::max<int64_t>(blocks, 1), 256, 0, stream, false, p,
                reinterpret_cast<uint4*>(p.pairs), count, info);
     if (e != cudaSuccess) return e;
   }
   const int64_t grid = p.in_order ? chains : std::min<int64_t>(chains * chunks, (int64_t)sms * S::kPerSm);
-  return launch(kernel, (unsigned)grid, 32 * (kWarps + 1), S::kSmem, stream, init, p);
+  return launch(kernel, (unsigned)grid, 32 * kWarps, S::kSmem, stream, init, p);
 }
 
 }  // namespace
@@ -812,7 +804,7 @@ size_t scan_workspace_bytes(int B, int T, int D, int N, int dtype) {
   const int64_t chains = (int64_t)B * div_up(D, kBlock), chunks = div_up(T, kMinRows);
   size_t bytes = 0;
   if (T > kInOrderRows)
-    bytes = ((size_t)(chains * chunks) * 64 + (size_t)(chains * div_up(chunks, kGroup)) * 32) * sizeof(float4);
+    bytes = (size_t)(chains * (2 * chunks + div_up(chunks, kGroup))) * kBlock * sizeof(float);
   if (N > 0) bytes += align256((size_t)T * 4);
   return bytes ? sizeof(WorkspaceHeader) + bytes : 0;
 }
