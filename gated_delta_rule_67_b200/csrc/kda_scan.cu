@@ -15,21 +15,24 @@
 // one sequence to the next, NaN included.
 //
 // What bounds it: bytes.  bf16 forward 6 B per element, backward 10-12, from
-// the 8-bit checkpoint 8.  So the data is read once, in one pass: a tile is
-// 128 channels (one scale block of the checkpoint) x L rows; each of 8 warps
-// holds R = L / 8 rows x 128 channels of a tile as alpha and input in
-// registers and folds them to (A, Bs).  Then one thread per channel folds the
-// 8 pairs and walks the state through them, so that each warp finds what
-// enters its rows and goes over them once more.  Tiles of one (batch, channel
-// block) chain are joined in the order of the rows: each tile publishes its
-// (A, Bs), the last of each group of kGroup tiles the state that leaves the
-// group; a tile folds the pairs of its group's earlier tiles onto the state
-// that left the group before.  The order of the fold is fixed, so the bits are
-// the same every time.  Tiles are drawn by ticket in the order of the rows, so
-// whatever a tile waits for belongs to a block that is running; the words of
-// the pairs are their own flags (all bits set = not yet written), so one trip
-// to L2 sees and fetches them.  While four warps do this, another draws the
-// next ticket and starts the tile after next on its way (TMA, three stages).
+// the 8-bit checkpoint 8.  So the data is read once, in one pass, in tiles of W
+// channels x L rows, narrow and tall (16 channels, one 32-byte sector of bf16)
+// so that there are many chains of tiles, one per (batch, W channels), and few
+// tiles in each.  A thread folds segments of 7 rows x 2 channels to (A, Bs),
+// alpha and the input staying in its registers; the segments are folded per
+// warp, the warps' pairs by one thread per channel, which also learns what
+// enters the tile; it goes back the same way, and each thread goes over its
+// segments once more.  Tiles of a chain are joined in the order of the rows.
+// Many chains (kManyChains), or short ones: a block walks a whole chain, and
+// what leaves a tile stays with it; one barrier per tile.  Few chains: tiles
+// are drawn by ticket in the order of the rows, so whatever a tile waits for
+// belongs to a block that is running; each tile publishes its (A, Bs), the
+// last of every kGroup tiles the state that leaves them, and a tile folds the
+// pairs of the earlier ones of its group onto the state that left the group
+// before; the words handed on are their own flags (all bits set = not yet
+// written), so one trip to L2 sees and fetches them.  The order of the fold
+// depends on the sizes alone, so the bits are the same every time.
+// The tile after next is on its way (TMA, three stages) while one is computed.
 #include <cudaTypedefs.h>
 #include <cuda_fp8.h>
 
@@ -44,23 +47,46 @@ namespace kda {
 namespace {
 
 using namespace sm100;
-constexpr int kBlock = 128;     // channels per tile and per scale of the checkpoint
+constexpr int kBlock = 128;     // channels per scale of the checkpoint
 constexpr int kWarps = 8;
-constexpr int kFeeder = 7;      // the warp that draws tickets and starts loads
-constexpr int kGroup = 16;      // tiles whose pairs are folded before a state is published
-constexpr int kStages = 3;
-constexpr int kInOrderRows = 256;  // chains of so few rows are walked by one block each
+constexpr int kThreads = 32 * kWarps;
+constexpr int kR = 7;           // rows of a segment: odd, so that the segments of a warp lie in different banks
+constexpr int kGroup = 16;      // few chains: tiles from one published state to the next
+constexpr int kManyChains = 128;   // from so many chains on, each is walked by one block
+constexpr int kInOrderRows = 512;  // and chains of so few rows are, too
+constexpr int kInfoPad = 512;   // rows of padding behind the packed sequences' row information
 constexpr uint32_t kEmpty = 0xffffffffu;     // a word not yet written
 constexpr uint32_t kPollLimit = 1u << 22;    // polls before a wait gives up
 constexpr uint32_t kBarLimit = 1u << 22;
 
-// exp(x) for x <= 126 ln 2, to about two ulp: 2^p for p = x / ln 2 rounded,
-// times 1 + (x - p ln 2), what the rounding left out.  x = -infinity gives NaN.
-__device__ __forceinline__ float exp_of(float x) {
-  const float p = x * 1.44269504f;
-  float e;
-  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(e) : "f"(p));
-  return fmaf(e, fmaf(p, -0.693147181f, x), e);
+// Two floats in one register pair: one instruction for both.
+using f2 = unsigned long long;
+__device__ __forceinline__ f2 pack(float x, float y) {
+  f2 r;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(x), "f"(y));
+  return r;
+}
+__device__ __forceinline__ void unpack(f2 v, float& x, float& y) { asm("mov.b64 {%0, %1}, %2;" : "=f"(x), "=f"(y) : "l"(v)); }
+__device__ __forceinline__ f2 both(float x) { return pack(x, x); }
+__device__ __forceinline__ f2 mul2(f2 a, f2 b) {
+  f2 r;
+  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+  return r;
+}
+__device__ __forceinline__ f2 add2(f2 a, f2 b) {
+  f2 r;
+  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+  return r;
+}
+__device__ __forceinline__ f2 fma2(f2 a, f2 b, f2 c) {
+  f2 r;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
+  return r;
+}
+__device__ __forceinline__ float ex2_of(float x) {
+  float r;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
+  return r;
 }
 __device__ __forceinline__ float rcp_of(float x) {
   float r;
@@ -77,31 +103,46 @@ __device__ __forceinline__ float min_nan(float a, float b) {
   asm("min.NaN.f32 %0, %1, %2;" : "=f"(r) : "f"(a), "f"(b));
   return r;
 }
-// 1 - exp(x) for x <= 0 given alpha = exp(x): the series where the difference
-// would lose the small rates that make the long memories.
-__device__ __forceinline__ float rate_of(float x, float alpha) {
-  float q = fmaf(x, 1.f / 40320.f, 1.f / 5040.f);
-  q = fmaf(x, q, 1.f / 720.f);
-  q = fmaf(x, q, 1.f / 120.f);
-  q = fmaf(x, q, 1.f / 24.f);
-  q = fmaf(x, q, 1.f / 6.f);
-  q = fmaf(x, q, 0.5f);
-  q = fmaf(x, q, 1.f);
-  return fabsf(x) < 0.5f ? -x * q : 1.f - alpha;
+// exp(x) for x <= 126 ln 2, to about two ulp: 2^p for p = x / ln 2 rounded,
+// times 1 + (x - p ln 2), what the rounding left out.  -infinity gives NaN.
+__device__ __forceinline__ f2 exp2_of(f2 x) {
+  const f2 p = mul2(x, both(1.44269504f));
+  float a, b;
+  unpack(p, a, b);
+  const f2 e = pack(ex2_of(a), ex2_of(b));
+  return fma2(e, fma2(p, both(-0.693147181f), x), e);
 }
-// alpha and 1 - alpha of a gate, each to a few ulp on its own.  The clamps
+// alpha and 1 - alpha of two gates, each to a few ulp on its own.  The clamps
 // keep the exponent's residual a number; past them exp is below 2^-126 and
-// counts as zero.  NaN stays NaN.
+// counts as zero.  NaN stays NaN.  For a given log-gate, 1 - alpha is the
+// series where the difference would lose the small rates that make the long
+// memories.
 template <bool RAW>
-__device__ __forceinline__ void gate(float g, float& alpha, float& beta) {
+__device__ __forceinline__ void gate(float g0, float g1, f2& alpha, f2& beta) {
   if (RAW) {
-    const float e = exp_of(-min_nan(fabsf(g), 128.f)), hi = rcp_of(1.f + e), lo = e * hi;
-    alpha = g >= 0.f ? hi : lo;
-    beta = g >= 0.f ? lo : hi;
+    const f2 e = exp2_of(pack(-min_nan(fabsf(g0), 128.f), -min_nan(fabsf(g1), 128.f)));
+    float s0, s1, l0, l1;
+    unpack(add2(e, both(1.f)), s0, s1);
+    s0 = rcp_of(s0), s1 = rcp_of(s1);
+    unpack(mul2(e, pack(s0, s1)), l0, l1);
+    const bool p0 = g0 >= 0.f, p1 = g1 >= 0.f;
+    alpha = pack(p0 ? s0 : l0, p1 ? s1 : l1);
+    beta = pack(p0 ? l0 : s0, p1 ? l1 : s1);
   } else {
-    const float x = max_nan(g, -128.f);
-    alpha = exp_of(x);
-    beta = rate_of(x, alpha);
+    const float x0 = max_nan(g0, -128.f), x1 = max_nan(g1, -128.f);
+    const f2 x = pack(x0, x1);
+    alpha = exp2_of(x);
+    f2 q = fma2(x, both(1.f / 40320.f), both(1.f / 5040.f));
+    q = fma2(x, q, both(1.f / 720.f));
+    q = fma2(x, q, both(1.f / 120.f));
+    q = fma2(x, q, both(1.f / 24.f));
+    q = fma2(x, q, both(1.f / 6.f));
+    q = fma2(x, q, both(0.5f));
+    q = fma2(x, q, both(1.f));
+    float a0, a1, q0, q1;
+    unpack(alpha, a0, a1);
+    unpack(mul2(x, q), q0, q1);
+    beta = pack(fabsf(x0) < 0.5f ? -q0 : 1.f - a0, fabsf(x1) < 0.5f ? -q1 : 1.f - a1);
   }
 }
 
@@ -128,54 +169,98 @@ __device__ __forceinline__ uint32_t encode4(const float* v, float inv) {
   const uint32_t hi = __nv_cvt_float2_to_fp8x2(make_float2(q[2], q[3]), __NV_SATFINITE, __NV_E4M3);
   return lo | hi << 16;
 }
-__device__ __forceinline__ void decode4(uint32_t c, float scale, float* v) {
-  const __half2 a = __half2(__nv_cvt_fp8x2_to_halfraw2((__nv_fp8x2_storage_t)(c & 0xffffu), __NV_E4M3));
-  const __half2 b = __half2(__nv_cvt_fp8x2_to_halfraw2((__nv_fp8x2_storage_t)(c >> 16), __NV_E4M3));
-  const float2 x = __half22float2(a), y = __half22float2(b);
-  v[0] = x.x * scale, v[1] = x.y * scale, v[2] = y.x * scale, v[3] = y.y * scale;
+__device__ __forceinline__ void decode2(uint16_t c, float scale, float* v) {
+  const float2 x = __half22float2(__half2(__nv_cvt_fp8x2_to_halfraw2(c, __NV_E4M3)));
+  v[0] = x.x * scale, v[1] = x.y * scale;
 }
 
-
-// ------------------------------------------------------------ four channels
-template <typename IO>
-__device__ __forceinline__ void lds4(const uint8_t* p, float* v) {
+// ----------------------------------------------- V = 2 or 4 channels of a row
+template <typename IO, int V>
+__device__ __forceinline__ void lds(const uint8_t* p, float* v) {
   if constexpr (sizeof(IO) == 4) {
-    const float4 q = *reinterpret_cast<const float4*>(p);
-    v[0] = q.x, v[1] = q.y, v[2] = q.z, v[3] = q.w;
+#pragma unroll
+    for (int j = 0; j < V; j += 2) {
+      const float2 q = reinterpret_cast<const float2*>(p)[j / 2];
+      v[j] = q.x, v[j + 1] = q.y;
+    }
   } else {
-    const uint2 q = *reinterpret_cast<const uint2*>(p);
-    v[0] = __uint_as_float(q.x << 16), v[1] = __uint_as_float(q.x & 0xffff0000u);
-    v[2] = __uint_as_float(q.y << 16), v[3] = __uint_as_float(q.y & 0xffff0000u);
+    uint32_t q[V / 2];
+    if constexpr (V == 4) {
+      const uint2 w = *reinterpret_cast<const uint2*>(p);
+      q[0] = w.x, q[1] = w.y;
+    } else {
+      q[0] = *reinterpret_cast<const uint32_t*>(p);
+    }
+#pragma unroll
+    for (int j = 0; j < V; j += 2) v[j] = __uint_as_float(q[j / 2] << 16), v[j + 1] = __uint_as_float(q[j / 2] & 0xffff0000u);
   }
 }
-template <typename IO>
-__device__ __forceinline__ void stg4(IO* p, const float* v, int n, bool vec) {
+// n: how many of them the row has; vec: its vectors are aligned and n is 0 or at least V.
+template <int V, typename IO>
+__device__ __forceinline__ void stg(IO* p, const float* v, int n, bool vec) {
   if (vec) {
     if (n <= 0) return;
     if constexpr (sizeof(IO) == 4) {
-      __stcs(reinterpret_cast<float4*>(p), make_float4(v[0], v[1], v[2], v[3]));
+      if constexpr (V == 4)
+        __stcs(reinterpret_cast<float4*>(p), make_float4(v[0], v[1], v[2], v[3]));
+      else
+        __stcs(reinterpret_cast<float2*>(p), make_float2(v[0], v[1]));
     } else {
-      const __nv_bfloat162 a = __floats2bfloat162_rn(v[0], v[1]), b = __floats2bfloat162_rn(v[2], v[3]);
-      __stcs(reinterpret_cast<uint2*>(p),
-             make_uint2(*reinterpret_cast<const uint32_t*>(&a), *reinterpret_cast<const uint32_t*>(&b)));
+      uint32_t w[V / 2];
+#pragma unroll
+      for (int j = 0; j < V; j += 2) {
+        const __nv_bfloat162 q = __floats2bfloat162_rn(v[j], v[j + 1]);
+        w[j / 2] = *reinterpret_cast<const uint32_t*>(&q);
+      }
+      if constexpr (V == 4)
+        __stcs(reinterpret_cast<uint2*>(p), make_uint2(w[0], w[1]));
+      else
+        __stcs(reinterpret_cast<uint32_t*>(p), w[0]);
     }
   } else {
 #pragma unroll
-    for (int j = 0; j < 4; ++j)
+    for (int j = 0; j < V; ++j)
       if (j < n) p[j] = from_f32<IO>(v[j]);
   }
 }
-__device__ __forceinline__ void ldg4(const float* p, float* v, int n, bool vec) {
+template <int V>
+__device__ __forceinline__ void ldg(const float* p, float* v, int n, bool vec) {
 #pragma unroll
-  for (int j = 0; j < 4; ++j) v[j] = 0.f;
+  for (int j = 0; j < V; ++j) v[j] = 0.f;
   if (!p || n <= 0) return;
   if (vec) {
-    const float4 q = *reinterpret_cast<const float4*>(p);
-    v[0] = q.x, v[1] = q.y, v[2] = q.z, v[3] = q.w;
+#pragma unroll
+    for (int j = 0; j < V; j += 2) {
+      const float2 q = reinterpret_cast<const float2*>(p)[j / 2];
+      v[j] = q.x, v[j + 1] = q.y;
+    }
   } else {
 #pragma unroll
-    for (int j = 0; j < 4; ++j)
+    for (int j = 0; j < V; ++j)
       if (j < n) v[j] = p[j];
+  }
+}
+template <int V>
+__device__ __forceinline__ void sts(float* p, const float* v) {
+  if constexpr (V == 4)
+    *reinterpret_cast<float4*>(p) = make_float4(v[0], v[1], v[2], v[3]);
+  else
+    *reinterpret_cast<float2*>(p) = make_float2(v[0], v[1]);
+}
+// fp32 or bf16 V channels from anywhere to this thread's place in shared
+// memory, asynchronously where 4-byte pieces are aligned.
+template <typename IO, int V>
+__device__ __forceinline__ void bring(uint8_t* dst, const IO* src, int n, bool words) {
+  IO* d = reinterpret_cast<IO*>(dst);
+  constexpr int kPer = 4 / sizeof(IO);  // channels per word
+#pragma unroll
+  for (int j = 0; j < V; j += kPer) {
+    if (words && j + kPer <= n) {
+      asm volatile("cp.async.ca.shared.global [%0], [%1], 4;" ::"r"(smem_u32(d + j)), "l"(src + j) : "memory");
+    } else {
+#pragma unroll
+      for (int i = j; i < j + kPer; ++i) d[i] = i < n ? src[i] : from_f32<IO>(0.f);
+    }
   }
 }
 
@@ -198,45 +283,62 @@ __device__ __forceinline__ uint32_t peek(const float* p) {
 // ------------------------------------------------------------------ the tiles
 enum Kind { kFwd, kFwdCkpt, kBwd, kBwdCkpt };
 
-// Input arrays of a stage, and rows per warp: a stage is 24 or 32 KiB, three
-// of them and two blocks per SM (the fp32 backward: 48 or 64 KiB, one block).
+// Tiles.  A lane holds V channels x U segments.  The forward that writes the
+// checkpoint needs a row's whole scale block in one warp: 128 channels x 56
+// rows, one segment per warp.  The others: 16 channels (32 from the
+// checkpoint, whose codes are one byte), segments side by side in a warp.
+// U and the stages keep two blocks' inputs within an SM's shared memory.
 template <Kind K, typename IO, bool COMPL>
 struct Shape {
   static constexpr bool kDown = K == kBwd || K == kBwdCkpt;
+  static constexpr bool kWide = K == kFwdCkpt;
+  static constexpr int V = kWide ? 4 : 2, W = kWide ? 128 : K == kBwdCkpt ? 32 : 16;
+  static constexpr int kAcross = W / V;                     // lanes of a row
+  static constexpr int U = (K == kFwd && sizeof(IO) == 2) || K == kBwdCkpt ? 2 : 1;
+  static constexpr int kSide = 32 / kAcross;                // segments side by side in a warp
+  static constexpr int kSegs = kSide * U;                   // of a warp
+  // Segments folded before the state goes on past them: those of a warp; the
+  // forward that writes the checkpoint keeps to the other's, so that short
+  // sequences, walked in order, get the same bits from both.
+  static constexpr int kFold = !kWide ? kSegs : sizeof(IO) == 2 ? 8 : 4;
+  static constexpr int kWarpRows = kSegs * kR, kL = kWarps * kWarpRows;
+  static constexpr int kBox = kL <= 256 ? kL : kL / 2;      // rows of one TMA copy
+  // input arrays: forward x, g; backward dy, g, h, x; from the checkpoint dy, lambda, z
   static constexpr int kIn = K == kBwd ? (COMPL ? 4 : 3) : K == kBwdCkpt ? 3 : 2;
-  static constexpr int kRows = sizeof(IO) == 4 || K == kBwd ? 4 : 8;  // per warp
-  static constexpr int kL = kWarps * kRows;
-  // element bytes of array i: forward x, g; backward dy, g, h, x; from the checkpoint dy, lambda, z
   __host__ __device__ static constexpr int eb(int i) { return K == kBwdCkpt && i > 0 ? 1 : (int)sizeof(IO); }
   __host__ __device__ static constexpr int at(int i) {
     int o = 0;
-    for (int j = 0; j < i; ++j) o += kL * kBlock * eb(j);
+    for (int j = 0; j < i; ++j) o += (kL * W * eb(j) + 127) / 128 * 128;
     return o;
   }
   static constexpr int kStage = at(kIn);
+  static constexpr int kStages = 3;
   static constexpr int kSmem = kStages * kStage;
-  static constexpr int kPerSm = kSmem > 96 * 1024 ? 1 : 2;
+  static constexpr int kPerSm = kSmem > 98304 ? 1 : 2;
 };
 
 struct TileArgs {
   ScanArgs a;
   CUtensorMap map[4];
   WorkspaceHeader* hdr;     // error word; pad[0] is the ticket
-  float* pairs;             // [chains][chunks][2][128]
-  float* states;            // [chains][groups][128]
+  float* pairs;             // [chains][chunks][2][W]
+  float* states;            // [chains][groups][W]
   const int32_t* info;      // packed: sequence * 4 + first * 2 + last of each row, -1 outside
   int chains, chunks, groups, blocks;  // blocks: of channels
-  bool tma, vec, in_order;
+  bool tma, vec, words, in_order;
 };
 
-struct __align__(16) Shared {
-  float pair[kWarps][2][kBlock];  // (A, Bs) of each warp's rows
-  float enter[kWarps][kBlock];    // what enters them
-  float carry[kBlock];            // in order: what leaves the tile
-  uint64_t full[kStages];
-  int tile[kStages];
-  int info[kStages][64];
-  uint8_t scale[kStages][2][64];
+template <typename S>
+struct __align__(128) Shared {
+  float seg[kWarps][S::kSegs][2][S::W];   // (A, Bs) of the segments (wide: in pair)
+  float enter[kWarps][S::kSegs][S::W];    // what enters them
+  float pair[2][kWarps][2][S::W];         // (A, Bs) of the warps, of two tiles (wide: of the segments)
+  float into[kWarps][S::W];               // few chains: what enters them
+  float carry[2][S::W];                   // in order: what leaves a tile
+  uint64_t full[S::kStages];
+  int4 tile[S::kStages];                  // chain, chunk (-1: none left), batch, channel block
+  int info[S::kStages][S::kL];
+  uint8_t scale[S::kStages][2][S::kL + 32];
 };
 
 struct Row {
@@ -245,20 +347,21 @@ struct Row {
 };
 
 template <Kind K, typename IO, bool RAW, bool COMPL>
-__global__ void __launch_bounds__(32 * kWarps, Shape<K, IO, COMPL>::kPerSm)
+__global__ void __launch_bounds__(kThreads, Shape<K, IO, COMPL>::kPerSm)
     scan_tile_kernel(const __grid_constant__ TileArgs p) {
   using S = Shape<K, IO, COMPL>;
-  constexpr int R = S::kRows, L = S::kL;
+  constexpr int V = S::V, W = S::W, U = S::U, L = S::kL, NS = S::kStages, NSEG = S::kSegs;
   constexpr bool kDown = S::kDown, kSave = K == kFwdCkpt, kFrom = K == kBwdCkpt;
   extern __shared__ __align__(128) uint8_t stages[];
-  __shared__ Shared sh;
+  __shared__ Shared<S> sh;
   const ScanArgs& a = p.a;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int side = lane / S::kAcross, across = lane % S::kAcross;
   const size_t rows = (size_t)a.B * a.T;
   const bool packed = a.cu != nullptr;
 
   if (threadIdx.x == 0) {
-    for (int s = 0; s < kStages; ++s) mbar_init(&sh.full[s], 2);
+    for (int s = 0; s < NS; ++s) mbar_init(&sh.full[s], 1);
     fence_mbar_init();
   }
   __syncthreads();
@@ -269,335 +372,440 @@ __global__ void __launch_bounds__(32 * kWarps, Shape<K, IO, COMPL>::kPerSm)
     atomicOr(&p.hdr->error, 1u);
     atomicExch(&p.hdr->where, where);
   };
-  auto first_row = [&](int chunk) { return (kDown ? p.chunks - 1 - chunk : chunk) * (int64_t)L; };
+  // where a tile lies
+  struct Place {
+    int chain, chunk, b, cb, c, n, s;  // batch, channel block; this lane's first channel, how many from it on; stage
+    int64_t t0;
+    uint8_t* st;
+  };
+  auto place_of = [&](int k, int4 tile) {
+    Place q;
+    q.chain = tile.x, q.chunk = tile.y, q.b = tile.z, q.cb = tile.w;
+    q.t0 = (kDown ? p.chunks - 1 - q.chunk : q.chunk) * (int64_t)L;
+    q.c = q.cb * W + across * V, q.n = a.D - q.c;
+    q.s = k % NS, q.st = stages + q.s * S::kStage;
+    return q;
+  };
+  const ScanCkptLayout lay = scan_ckpt_layout(rows, a.D);
+  auto scale_at = [&](const Place& q) { return (size_t)(q.cb * W / kBlock) * rows + (size_t)q.b * a.T + q.t0; };
 
-  // ---- the feeder: tile `it` of this block into its stage
-  uint32_t drawn = 0;  // lane 0: the next ticket
-  if (warp == kFeeder && lane == 0 && !p.in_order) drawn = atomicAdd(&p.hdr->pad[0], 1u);
-  bool fed_all = false;
-  auto feed = [&](int it) {
-    if (fed_all) return;
-    const int s = it % kStages;
-    int tile;
-    if (p.in_order) {
-      tile = it < p.chunks ? it * p.chains + (int)blockIdx.x : -1;
+  // ---- warp 0, lane 0: the k-th tile of this block into its stage
+  uint32_t drawn = 0;  // the next ticket
+  int4 next = make_int4((int)blockIdx.x, 0, (int)blockIdx.x / p.blocks, (int)blockIdx.x % p.blocks);
+  if (threadIdx.x == 0 && !p.in_order) drawn = atomicAdd(&p.hdr->pad[0], 1u);
+  auto feed = [&](int k) {
+    if (next.y < 0) return;
+    const int s = k % NS;
+    if (!p.in_order) {
+      const bool there = drawn < (uint32_t)p.chains * (uint32_t)p.chunks;
+      next.y = there ? (int)(drawn / (uint32_t)p.chains) : -1;
+      next.x = (int)(drawn % (uint32_t)p.chains);
+      next.z = next.x / p.blocks, next.w = next.x % p.blocks;
+      if (there) drawn = atomicAdd(&p.hdr->pad[0], 1u);
     } else {
-      const uint32_t t = __shfl_sync(0xffffffffu, drawn, 0);
-      tile = t < (uint32_t)p.chains * (uint32_t)p.chunks ? (int)t : -1;
-      if (tile >= 0 && lane == 0) drawn = atomicAdd(&p.hdr->pad[0], 1u);
+      next.y = k < p.chunks ? k : -1;
     }
-    if (lane == 0) sh.tile[s] = tile;
-    if (tile < 0) {
-      if (lane == 0) mbar_arrive(&sh.full[s]), mbar_arrive(&sh.full[s]);
-      fed_all = true;
+    sh.tile[s] = next;
+    if (next.y < 0) {
+      mbar_arrive(&sh.full[s]);
       return;
     }
-    const int chain = tile % p.chains, chunk = tile / p.chains, b = chain / p.blocks, cb = chain % p.blocks;
-    const int64_t t0 = first_row(chunk);
-    if (lane == 0 && p.tma) {
-      mbar_expect_tx(&sh.full[s], S::kStage);
-#pragma unroll
-      for (int i = 0; i < S::kIn; ++i)  // h one row up: what enters each row
-        tma_load_3d(stages + s * S::kStage + S::at(i), &p.map[i], &sh.full[s], cb * kBlock,
-                    (int)t0 - (K == kBwd && i == 2 ? 1 : 0), b);
-    }
-    if (packed)
-      for (int i = lane; i < L; i += 32) sh.info[s][i] = t0 + i < a.T ? p.info[t0 + i] : -1;
+    const Place q = place_of(k, next);
+    constexpr uint32_t kArray = L * W * sizeof(IO);  // an array in the caller's type
+    uint32_t bytes = (p.tma ? (kFrom ? 1 : S::kIn) * kArray : 0) + (kFrom ? 2 * L * W : 0) + (packed ? L * 4 : 0);
+    uint32_t scale_bytes = 0;
     if (kFrom) {
-      const ScanCkptLayout l = scan_ckpt_layout(rows, a.D);
-      for (int i = lane; i < L; i += 32) {
-        const size_t at = cb * rows + (size_t)b * a.T + t0 + i;
-        sh.scale[s][0][i] = t0 + i < a.T ? a.ckpt[l.lam_scale + at] : 1;
-        sh.scale[s][1][i] = t0 + i < a.T ? a.ckpt[l.z_scale + at] : 1;
-      }
+      const uint32_t valid = (uint32_t)min((int64_t)L, a.T - q.t0);
+      scale_bytes = ((uint32_t)(scale_at(q) & 15) + valid + 15) & ~15u;
+      bytes += 2 * scale_bytes;
     }
-    __syncwarp();
-    if (lane == 0) mbar_arrive(&sh.full[s]);
-    if (lane == 0 && !p.tma) mbar_arrive(&sh.full[s]);
+    if (bytes)
+      mbar_expect_tx(&sh.full[s], bytes);
+    else
+      mbar_arrive(&sh.full[s]);
+#pragma unroll
+    for (int i = 0; i < S::kIn; ++i)
+      if (p.tma || (kFrom && i > 0))
+#pragma unroll
+        for (int part = 0; part < L / S::kBox; ++part)  // h one row up: what enters each row
+          tma_load_3d(q.st + S::at(i) + part * S::kBox * W * S::eb(i), &p.map[i], &sh.full[s], q.cb * W,
+                      (int)q.t0 + part * S::kBox - (K == kBwd && i == 2 ? 1 : 0), q.b);
+    if (packed) bulk_load(sh.info[s], p.info + q.t0, L * 4, &sh.full[s]);
+    if (kFrom) {
+      const size_t at = scale_at(q) & ~size_t(15);
+      bulk_load(sh.scale[s][0], a.ckpt + lay.lam_scale + at, scale_bytes, &sh.full[s]);
+      bulk_load(sh.scale[s][1], a.ckpt + lay.z_scale + at, scale_bytes, &sh.full[s]);
+    }
   };
-  if (warp == kFeeder) feed(0), feed(1);
+  if (threadIdx.x == 0) feed(0), feed(1);
+
+  // the k-th tile of this block, chunk -1 past its last
+  auto tile_of = [&](int k) {
+    const bool there = mbar_wait(&sh.full[k % NS], (k / NS) & 1, kBarLimit);
+    if (!there) gave_up(202);
+    return there ? sh.tile[k % NS] : make_int4(0, -1, 0, 0);
+  };
+  // row of the tile: r-th of this lane's u-th segment; segments are numbered in the order of the recurrence
+  auto seg_of = [&](int u) { return u * S::kSide + side; };
+  auto row_at = [&](int u, int r) {
+    const int i = warp * S::kWarpRows + seg_of(u) * kR + r;
+    return kDown ? L - 1 - i : i;
+  };
+  auto elem = [&](const Place& q, int arr, int i) { return q.st + S::at(arr) + (i * W + across * V) * S::eb(arr); };
+  auto global_row = [&](const Place& q, int i) { return (size_t)q.b * a.T + q.t0 + i; };
+  auto row_info = [&](const Place& q, int i) {
+    Row o;
+    if (packed) {
+      const int v = sh.info[q.s][i];
+      o.valid = v >= 0, o.first = v & 2, o.last = v & 1, o.seq = v >> 2;
+    } else {
+      const int64_t t = q.t0 + i;
+      o.valid = t < a.T, o.first = t == 0, o.last = t == a.T - 1, o.seq = q.b;
+    }
+    return o;
+  };
+  // whether any of the warp's rows starts or ends a sequence or belongs to none
+  auto has_edge = [&](const Place& q) {
+    const int lo = kDown ? L - (warp + 1) * S::kWarpRows : warp * S::kWarpRows;
+    if (!packed) return q.t0 + lo == 0 || q.t0 + lo + S::kWarpRows >= a.T;
+    bool edge = false;
+    for (int i = lane; i < S::kWarpRows; i += 32) {
+      const int v = sh.info[q.s][lo + i];
+      edge |= v < 0 || (v & 3);
+    }
+    return __any_sync(0xffffffffu, edge) != 0;
+  };
+  auto state_of = [&](const Place& q, const float* base, int seq, float* v) {
+    ldg<V>(base ? base + (size_t)seq * a.D + q.c : nullptr, v, q.n, p.vec);
+  };
+  auto codes_of = [&](const Place& q, int arr, int i, float* v) {
+    decode2(*reinterpret_cast<const uint16_t*>(elem(q, arr, i)), pow2(sh.scale[q.s][arr - 1][(scale_at(q) & 15) + i]), v);
+  };
+  auto load_gate = [&](const Place& q, int i, float* g) {
+    if constexpr (kFrom)
+      codes_of(q, 1, i, g);
+    else
+      lds<IO, V>(elem(q, 1, i), g);
+  };
+  // rows that TMA cannot take (their pitch is no multiple of 16 bytes): each lane brings its own channels of tile k
+  auto bring_tile = [&](int k) {
+    const int4 tile = tile_of(k);
+    if (tile.y >= 0) {
+      const Place q = place_of(k, tile);
+#pragma unroll
+      for (int u = 0; u < U; ++u)
+        for (int r = 0; r < kR; ++r) {
+          const int i = row_at(u, r);
+          const bool in = q.t0 + i < a.T && q.n > 0;
+#pragma unroll
+          for (int arr = 0; arr < (kFrom ? 1 : S::kIn); ++arr) {
+            const void* src = !kDown ? (arr == 0 ? a.x : a.g) : (arr == 0 ? a.dy : arr == 1 ? a.g : arr == 2 ? a.h : a.x);
+            const bool up = K == kBwd && arr == 2;
+            const bool ok = in && (!up || q.t0 + i > 0);
+            bring<IO, V>(elem(q, arr, i), static_cast<const IO*>(src) + (ok ? (global_row(q, i) - up) * a.D + q.c : 0),
+                         ok ? q.n : 0, p.words);
+          }
+        }
+    }
+    asm volatile("cp.async.commit_group;" ::: "memory");
+  };
+  if (!p.tma) bring_tile(0);
 
   bool failed = false;
-  for (int it = 0;; ++it) {
-    const int s = it % kStages;
-    const bool there = mbar_wait(&sh.full[s], (it / kStages) & 1, kBarLimit);
-    if (!there) gave_up(202);
-    const int tile = there ? sh.tile[s] : -1;
-    if (tile < 0) break;
-    const int chain = tile % p.chains, chunk = tile / p.chains, b = chain / p.blocks, cb = chain % p.blocks;
-    const int64_t t0 = first_row(chunk);
-    const int c = cb * kBlock + lane * 4, n = a.D - c;  // this lane's channels, and how many there are (from 4 up: 4)
-    uint8_t* st = stages + s * S::kStage;
-    // row i of the tile that this warp handles r-th
-    auto row_at = [&](int r) { return kDown ? L - 1 - (warp * R + r) : warp * R + r; };
-    auto elem = [&](int arr, int i) { return st + S::at(arr) + (i * kBlock + lane * 4) * S::eb(arr); };
-    auto global_row = [&](int i) { return (size_t)b * a.T + t0 + i; };
-
+  for (int k = 0;; ++k) {
+    const int4 tile = tile_of(k);
+    if (tile.y < 0) break;
     if (!p.tma) {
-      // rows that TMA cannot take: each lane brings its own four channels
-      for (int r = 0; r < R; ++r) {
-        const int i = row_at(r);
-        const bool in = t0 + i < a.T;
-#pragma unroll
-        for (int arr = 0; arr < S::kIn; ++arr) {
-          if (kFrom && arr > 0) {
-            const ScanCkptLayout l = scan_ckpt_layout(rows, a.D);
-            uint32_t v = 0;
-            if (in && n > 0)
-              v = *reinterpret_cast<const uint32_t*>(a.ckpt + (arr == 2 ? l.z : 0) + global_row(i) * l.pitch + c);
-            *reinterpret_cast<uint32_t*>(elem(arr, i)) = v;
-            continue;
-          }
-          const void* src = K == kFwd || K == kFwdCkpt ? (arr == 0 ? a.x : a.g)
-                                                       : (arr == 0 ? a.dy : arr == 1 ? a.g : arr == 2 ? a.h : a.x);
-          const bool up = K == kBwd && arr == 2;
-          const bool ok = in && (!up || t0 + i > 0);
-          const IO* q = static_cast<const IO*>(src) + (ok ? (global_row(i) - up) * a.D + c : 0);
-          IO* d = reinterpret_cast<IO*>(elem(arr, i));
-#pragma unroll
-          for (int j = 0; j < 4; ++j) d[j] = ok && j < n ? q[j] : from_f32<IO>(0.f);
-        }
-      }
-      __syncwarp();
+      bring_tile(k + 1);
+      asm volatile("cp.async.wait_group 1;" ::: "memory");
     }
+    const Place q = place_of(k, tile);
+    const bool edge = has_edge(q);
+    float(*pair)[2][W] = sh.pair[k & 1];
 
-    auto row_info = [&](int i) {
-      Row q;
-      if (packed) {
-        const int v = sh.info[s][i];
-        q.valid = v >= 0, q.first = v & 2, q.last = v & 1, q.seq = v >> 2;
-      } else {
-        const int64_t t = t0 + i;
-        q.valid = t < a.T, q.first = t == 0, q.last = t == a.T - 1, q.seq = b;
-      }
-      return q;
-    };
-    // whether any of the warp's rows starts or ends a sequence or belongs to none
-    bool edge = false;
-    if (lane < R) {
-      const Row q = row_info(row_at(lane));
-      edge = !q.valid || q.first || q.last;
-    }
-    edge = __any_sync(0xffffffffu, edge);
-    auto state_of = [&](const float* base, int seq, float* v) {
-      ldg4(base ? base + (size_t)seq * a.D + c : nullptr, v, n, p.vec);
-    };
-    auto load_gate = [&](int i, float* g) {
-      if constexpr (kFrom)
-        decode4(*reinterpret_cast<const uint32_t*>(elem(1, i)), pow2(sh.scale[s][0][i]), g);
-      else
-        lds4<IO>(elem(1, i), g);
-    };
-
-    // ---- the warp's rows as one pair
-    float al[R][4], u[R][4];  // alpha; forward: the input, backward: 1 - alpha
-    float A[4], B[4];
+    // ---- segments as pairs
+    f2 al[U][kR][V / 2], in[U][kR][V / 2];  // alpha; forward: the input, backward: 1 - alpha
     auto reduce = [&](auto edges) {
+      constexpr bool E = decltype(edges)::value;
 #pragma unroll
-      for (int j = 0; j < 4; ++j) A[j] = 1.f, B[j] = 0.f;
+      for (int u = 0; u < U; ++u) {
+        f2 A[V / 2], B[V / 2];
 #pragma unroll
-      for (int r = 0; r < R; ++r) {
-        const int i = row_at(r);
-        float g[4], v[4];
-        load_gate(i, g);
-        lds4<IO>(elem(0, i), v);
-        const Row q = edges.value ? row_info(i) : Row{true, false, false, 0};
-        float from[4];
-        const bool start = edges.value && q.valid && (kDown ? q.last : q.first);
-        if (start) state_of(a.s0, q.seq, from);
+        for (int j = 0; j < V / 2; ++j) A[j] = both(1.f), B[j] = both(0.f);
 #pragma unroll
-        for (int j = 0; j < 4; ++j) {
-          float be;
-          gate<RAW && !kFrom>(g[j], al[r][j], be);
-          u[r][j] = kDown ? be : COMPL ? be * v[j] : v[j];
-          if (edges.value && !q.valid) continue;
-          if (start) {
-            if (!kDown) u[r][j] = fmaf(al[r][j], from[j], u[r][j]);
-            A[j] = -0.f;
-            B[j] = kDown ? al[r][j] * (v[j] + from[j]) : u[r][j];
-          } else {
-            A[j] *= al[r][j];
-            B[j] = kDown ? al[r][j] * (B[j] + v[j]) : fmaf(al[r][j], B[j], u[r][j]);
+        for (int r = 0; r < kR; ++r) {
+          const int i = row_at(u, r);
+          float g[V], v[V], from[V];
+          load_gate(q, i, g);
+          lds<IO, V>(elem(q, 0, i), v);
+          const Row o = E ? row_info(q, i) : Row{true, false, false, 0};
+          const bool start = E && o.valid && (kDown ? o.last : o.first);
+          if (start) state_of(q, a.s0, o.seq, from);
+#pragma unroll
+          for (int j = 0; j < V / 2; ++j) {
+            f2 be;
+            gate<RAW && !kFrom>(g[2 * j], g[2 * j + 1], al[u][r][j], be);
+            const f2 x = pack(v[2 * j], v[2 * j + 1]);
+            in[u][r][j] = kDown ? be : COMPL ? mul2(be, x) : x;
+            if (E && !o.valid) continue;
+            if (start) {
+              const f2 f = pack(from[2 * j], from[2 * j + 1]);
+              if (!kDown) in[u][r][j] = fma2(al[u][r][j], f, in[u][r][j]);
+              A[j] = both(-0.f);
+              B[j] = kDown ? mul2(al[u][r][j], add2(x, f)) : in[u][r][j];
+            } else {
+              A[j] = mul2(A[j], al[u][r][j]);
+              B[j] = kDown ? mul2(al[u][r][j], add2(B[j], x)) : fma2(al[u][r][j], B[j], in[u][r][j]);
+            }
           }
         }
+        float(*to)[W] = S::kWide ? pair[warp] : sh.seg[warp][seg_of(u)];
+        float f[V];
+#pragma unroll
+        for (int j = 0; j < V / 2; ++j) unpack(A[j], f[2 * j], f[2 * j + 1]);
+        sts<V>(&to[0][across * V], f);
+#pragma unroll
+        for (int j = 0; j < V / 2; ++j) unpack(B[j], f[2 * j], f[2 * j + 1]);
+        sts<V>(&to[1][across * V], f);
       }
     };
     if (edge)
       reduce(std::true_type{});
     else
       reduce(std::false_type{});
-    *reinterpret_cast<float4*>(&sh.pair[warp][0][lane * 4]) = make_float4(A[0], A[1], A[2], A[3]);
-    *reinterpret_cast<float4*>(&sh.pair[warp][1][lane * 4]) = make_float4(B[0], B[1], B[2], B[3]);
-    __syncthreads();  // the pairs are there, and every warp is done with the tile before
-
-    // ---- what enters each warp's rows: one thread per channel
-    const int place = chunk % kGroup;
-    if (warp < kBlock / 32) {
-      const int ch = threadIdx.x;
-      float* pairs = p.pairs + ((size_t)chain * p.chunks + chunk) * (2 * kBlock) + ch;
-      if (!p.in_order && place != kGroup - 1 && chunk != p.chunks - 1) {
-        float ta = sh.pair[0][0][ch], tb = sh.pair[0][1][ch];
+    if constexpr (!S::kWide) {  // the warp's pair
+      __syncwarp();
+      if (lane < W) {
+        float ta = sh.seg[warp][0][0][lane], tb = sh.seg[warp][0][1][lane];
 #pragma unroll
-        for (int w = 1; w < kWarps; ++w) {
-          const float wa = sh.pair[w][0][ch], wb = sh.pair[w][1][ch];
+        for (int g = 1; g < NSEG; ++g) {
+          const float wa = sh.seg[warp][g][0][lane], wb = sh.seg[warp][g][1][lane];
           tb = through(tb, wa, wb);
           ta = fresh(wa) ? wa : ta * wa;
         }
-        publish(pairs, ta);
-        publish(pairs + kBlock, tb);
+        pair[warp][0][lane] = ta, pair[warp][1][lane] = tb;
       }
-      float h = 0.f;
-      if (p.in_order) {
-        if (chunk > 0) h = sh.carry[ch];
-      } else {
-        auto arrived = [&](const float* q, uint32_t v) {
+    }
+    __syncthreads();  // the pairs are there, and every warp is done with the tile before
+    if (threadIdx.x == 0) feed(k + 2);  // into its stage
+
+    // ---- what enters the warps, from what enters the tile: one thread per channel
+    if (!p.in_order) {
+      const int place = q.chunk % kGroup;
+      if (warp < (W + 31) / 32) {  // with 16 channels both halves of the warp do the same
+        const int ch = threadIdx.x % W;
+        float* state = p.states + ((size_t)q.chain * p.groups + q.chunk / kGroup) * W + ch;
+        float* pairs = p.pairs + ((size_t)q.chain * p.chunks + q.chunk) * (2 * W) + ch;
+        auto arrived = [&](const float* at, uint32_t v) {
           for (uint32_t i = 0; v == kEmpty; ++i) {
             if (i >= (failed ? 1u : kPollLimit)) {
               failed = true;
               gave_up(203);
               break;
             }
-            v = peek(q);
+            v = peek(at);
           }
           return __uint_as_float(v);
         };
-        const float* head = p.states + ((size_t)chain * p.groups + chunk / kGroup - 1) * kBlock + ch;
-        uint32_t hv = 0, va[kGroup - 1], vb[kGroup - 1];
-        if (chunk >= kGroup) hv = peek(head);
-        const float* q = pairs - (size_t)place * (2 * kBlock);
+        uint32_t head = 0;
+        if (q.chunk >= kGroup) head = peek(state - W);
+        float ta = pair[0][0][ch], tb = pair[0][1][ch];
 #pragma unroll
-        for (int k = 0; k < kGroup - 1; ++k)
-          if (k < place) va[k] = peek(q + k * 2 * kBlock), vb[k] = peek(q + (k * 2 + 1) * kBlock);
-        if (chunk >= kGroup) h = arrived(head, hv);
+        for (int w = 1; w < kWarps; ++w) {
+          const float wa = pair[w][0][ch], wb = pair[w][1][ch];
+          tb = through(tb, wa, wb);
+          ta = fresh(wa) ? wa : ta * wa;
+        }
+        if (place != kGroup - 1 && q.chunk != p.chunks - 1) publish(pairs, ta), publish(pairs + W, tb);
+        float ga = 1.f, gb = 0.f;  // the group's earlier tiles
+        constexpr int kBatch = 5;
+        for (int k0 = 0; k0 < place; k0 += kBatch) {
+          const float* at = pairs - (size_t)(place - k0) * (2 * W);
+          uint32_t va[kBatch], vb[kBatch];
 #pragma unroll
-        for (int k = 0; k < kGroup - 1; ++k)
-          if (k < place) {
-            const float ka = arrived(q + k * 2 * kBlock, va[k]), kb = arrived(q + (k * 2 + 1) * kBlock, vb[k]);
-            h = through(h, ka, kb);
+          for (int i = 0; i < kBatch; ++i)
+            if (k0 + i < place) va[i] = peek(at + i * 2 * W), vb[i] = peek(at + i * 2 * W + W);
+#pragma unroll
+          for (int i = 0; i < kBatch; ++i)
+            if (k0 + i < place) {
+              const float ka = arrived(at + i * 2 * W, va[i]), kb = arrived(at + i * 2 * W + W, vb[i]);
+              gb = through(gb, ka, kb);
+              ga = fresh(ka) ? ka : ga * ka;
+            }
+        }
+        float h = q.chunk >= kGroup ? arrived(state - W, head) : 0.f;
+        h = through(h, ga, gb);
+        if (place == kGroup - 1) publish(state, through(h, ta, tb));
+#pragma unroll
+        for (int w = 0; w < kWarps; ++w) {
+          sh.into[w][ch] = h;
+          h = through(h, pair[w][0][ch], pair[w][1][ch]);
+        }
+      }
+      __syncthreads();
+    }
+    if constexpr (S::kWide) {
+#pragma unroll
+      for (int j = 0; j < V; ++j) {
+        const int ch = lane * V + j;
+        float h;
+        if (!p.in_order) {
+          h = sh.into[warp][ch];
+        } else {
+          // carry through the earlier folds of the tile, then segment by segment
+          h = k > 0 ? sh.carry[k & 1][ch] : 0.f;
+          float fa = 1.f, fb = 0.f;
+          for (int w = 0; w < kWarps; ++w) {
+            if (w >= warp && warp != kWarps - 1) break;
+            const float wa = pair[w][0][ch], wb = pair[w][1][ch];
+            fb = w % S::kFold == 0 ? wb : through(fb, wa, wb);
+            fa = w % S::kFold == 0 || fresh(wa) ? wa : fa * wa;
+            if (w % S::kFold == S::kFold - 1) {
+              if (w < warp) h = through(h, fa, fb);
+              else sh.carry[(k + 1) & 1][ch] = through(h, fa, fb);
+            }
           }
+          for (int w = warp / S::kFold * S::kFold; w < warp; ++w) h = through(h, pair[w][0][ch], pair[w][1][ch]);
+        }
+        sh.enter[warp][0][ch] = h;
+      }
+    } else if (lane < W) {
+      float h;
+      if (!p.in_order) {
+        h = sh.into[warp][lane];
+      } else {
+        h = k > 0 ? sh.carry[k & 1][lane] : 0.f;
+        for (int w = 0; w < warp; ++w) h = through(h, pair[w][0][lane], pair[w][1][lane]);
+        if (warp == kWarps - 1) sh.carry[(k + 1) & 1][lane] = through(h, pair[warp][0][lane], pair[warp][1][lane]);
       }
 #pragma unroll
-      for (int w = 0; w < kWarps; ++w) {
-        sh.enter[w][ch] = h;
-        h = through(h, sh.pair[w][0][ch], sh.pair[w][1][ch]);
+      for (int g = 0; g < NSEG; ++g) {
+        sh.enter[warp][g][lane] = h;
+        h = through(h, sh.seg[warp][g][0][lane], sh.seg[warp][g][1][lane]);
       }
-      if (p.in_order)
-        sh.carry[ch] = h;
-      else if (place == kGroup - 1)
-        publish(p.states + ((size_t)chain * p.groups + chunk / kGroup) * kBlock + ch, h);
-    } else if (warp == kFeeder) {
-      feed(it + 2);  // into the stage of the tile before this one
     }
-    __syncthreads();
-    float h[4];  // the state that enters (forward), c_{t+1} (backward)
-    {
-      const float4 q = *reinterpret_cast<const float4*>(&sh.enter[warp][lane * 4]);
-      h[0] = q.x, h[1] = q.y, h[2] = q.z, h[3] = q.w;
-    }
+    __syncwarp();
 
     // ---- the rows themselves
-    int lam_code = 0, z_code = 0;  // of row `lane` of the warp
+    const int64_t step = kDown ? -(int64_t)a.D : (int64_t)a.D;
     auto emit = [&](auto edges) {
+      constexpr bool E = decltype(edges)::value;
+      int lam_code = 0, z_code = 0;  // of the warp's row `lane`
 #pragma unroll
-      for (int r = 0; r < R; ++r) {
-        const int i = row_at(r);
-        const Row q = edges.value ? row_info(i) : Row{true, false, false, 0};
-        if (edges.value && !q.valid) {
-          if (packed && t0 + i < a.T) {  // a row that no sequence owns
-            const float zero[4] = {0.f, 0.f, 0.f, 0.f};
-            stg4(static_cast<IO*>(a.out) + global_row(i) * a.D + c, zero, n, p.vec);
-            if (kDown) stg4(static_cast<IO*>(a.dg) + global_row(i) * a.D + c, zero, n, p.vec);
-            if (kSave) {
-              const ScanCkptLayout l = scan_ckpt_layout(rows, a.D);
-              if (n > 0) {
-                *reinterpret_cast<uint32_t*>(a.ckpt + global_row(i) * l.pitch + c) = 0;
-                *reinterpret_cast<uint32_t*>(a.ckpt + l.z + global_row(i) * l.pitch + c) = 0;
-              }
-              if (lane == r) lam_code = z_code = 1;
-            }
-          }
-          continue;
+      for (int u = 0; u < U; ++u) {
+        f2 h[V / 2];  // the state that enters (forward), c_{t+1} (backward)
+        {
+          float f[V];
+          lds<float, V>(reinterpret_cast<const uint8_t*>(&sh.enter[warp][seg_of(u)][across * V]), f);
+#pragma unroll
+          for (int j = 0; j < V / 2; ++j) h[j] = pack(f[2 * j], f[2 * j + 1]);
         }
-        const bool start = edges.value && (kDown ? q.last : q.first);
-        if constexpr (!kDown) {
-          float z[4], lam[4];
-          if constexpr (kSave) {
-            float g[4];
-            load_gate(i, g);
-            if (start)
-              state_of(a.s0, q.seq, z);
-            else
+        const size_t from_row = global_row(q, row_at(u, 0));
+        IO* out = static_cast<IO*>(a.out) + from_row * a.D + q.c;
+        IO* out2 = static_cast<IO*>(a.dg) + (kDown ? from_row * a.D + q.c : 0);
 #pragma unroll
-              for (int j = 0; j < 4; ++j) z[j] = h[j];
-            if (COMPL) {
-              float x[4];
-              lds4<IO>(elem(0, i), x);
+        for (int r = 0; r < kR; ++r, out += step, out2 += step) {
+          const int i = row_at(u, r);
+          const Row o = E ? row_info(q, i) : Row{true, false, false, 0};
+          if (E && !o.valid) {
+            if (packed && q.t0 + i < a.T) {  // a row that no sequence owns
+              float zero[V];
 #pragma unroll
-              for (int j = 0; j < 4; ++j) z[j] -= x[j];
+              for (int j = 0; j < V; ++j) zero[j] = 0.f;
+              stg<V>(out, zero, q.n, p.vec);
+              if (kDown) stg<V>(out2, zero, q.n, p.vec);
+              if (kSave) {
+                if (q.n > 0) {
+                  *reinterpret_cast<uint32_t*>(a.ckpt + global_row(q, i) * lay.pitch + q.c) = 0;
+                  *reinterpret_cast<uint32_t*>(a.ckpt + lay.z + global_row(q, i) * lay.pitch + q.c) = 0;
+                }
+                if (lane == r) lam_code = z_code = 1;
+              }
+            }
+            continue;
+          }
+          const bool start = E && (kDown ? o.last : o.first);
+          float w[V];  // what is stored
+          if constexpr (!kDown) {
+            [[maybe_unused]] float z[V], lam[V];
+            if constexpr (kSave) {
+              float g[V], x[V];
+              load_gate(q, i, g);
+              if (start)
+                state_of(q, a.s0, o.seq, z);
+              else
+#pragma unroll
+                for (int j = 0; j < V / 2; ++j) unpack(h[j], z[2 * j], z[2 * j + 1]);
+              if (COMPL) {
+                lds<IO, V>(elem(q, 0, i), x);
+#pragma unroll
+                for (int j = 0; j < V; ++j) z[j] -= x[j];
+              }
+#pragma unroll
+              for (int j = 0; j < V; ++j) lam[j] = !RAW ? g[j] : j < q.n ? log_sigmoid(g[j]) : 0.f;
             }
 #pragma unroll
-            for (int j = 0; j < 4; ++j) lam[j] = !RAW ? g[j] : j < n ? log_sigmoid(g[j]) : 0.f;
-          }
-#pragma unroll
-          for (int j = 0; j < 4; ++j) h[j] = start ? u[r][j] : fmaf(al[r][j], h[j], u[r][j]);
-          stg4(static_cast<IO*>(a.out) + global_row(i) * a.D + c, h, n, p.vec);
-          if constexpr (kSave) {
-            const ScanCkptLayout l = scan_ckpt_layout(rows, a.D);
-            uint32_t ml = 0, mz = 0;
-#pragma unroll
-            for (int j = 0; j < 4; ++j) ml = max(ml, magnitude(lam[j])), mz = max(mz, magnitude(z[j]));
-            const int kl = scale_code(__uint_as_float(__reduce_max_sync(0xffffffffu, ml)));
-            const int kz = scale_code(__uint_as_float(__reduce_max_sync(0xffffffffu, mz)));
-            if (n > 0) {
-              *reinterpret_cast<uint32_t*>(a.ckpt + global_row(i) * l.pitch + c) = encode4(lam, pow2(254 - kl));
-              *reinterpret_cast<uint32_t*>(a.ckpt + l.z + global_row(i) * l.pitch + c) = encode4(z, pow2(254 - kz));
+            for (int j = 0; j < V / 2; ++j) {
+              h[j] = start ? in[u][r][j] : fma2(al[u][r][j], h[j], in[u][r][j]);
+              unpack(h[j], w[2 * j], w[2 * j + 1]);
             }
-            if (lane == r) lam_code = kl, z_code = kz;
-          }
-          if (edges.value && q.last && a.sT) {
+            stg<V>(out, w, q.n, p.vec);
+            if constexpr (kSave) {
+              uint32_t ml = 0, mz = 0;
 #pragma unroll
-            for (int j = 0; j < 4; ++j)
-              if (j < n) a.sT[(size_t)q.seq * a.D + c + j] = h[j];
-          }
-        } else {
-          float z[4], v[4], dx[4], dg[4], from[4];
-          lds4<IO>(elem(0, i), v);
-          if (start) state_of(a.s0, q.seq, from);
-          if constexpr (kFrom) {
-            decode4(*reinterpret_cast<const uint32_t*>(elem(2, i)), pow2(sh.scale[s][1][i]), z);
+              for (int j = 0; j < V; ++j) ml = max(ml, magnitude(lam[j])), mz = max(mz, magnitude(z[j]));
+              const int kl = scale_code(__uint_as_float(__reduce_max_sync(0xffffffffu, ml)));
+              const int kz = scale_code(__uint_as_float(__reduce_max_sync(0xffffffffu, mz)));
+              if (q.n > 0) {
+                *reinterpret_cast<uint32_t*>(a.ckpt + global_row(q, i) * lay.pitch + q.c) = encode4(lam, pow2(254 - kl));
+                *reinterpret_cast<uint32_t*>(a.ckpt + lay.z + global_row(q, i) * lay.pitch + q.c) = encode4(z, pow2(254 - kz));
+              }
+              if (lane == r) lam_code = kl, z_code = kz;
+            }
           } else {
-            if (edges.value && q.first)
-              state_of(a.h0, q.seq, z);
-            else
-              lds4<IO>(elem(2, i), z);
-            if (COMPL) {
-              float x[4];
-              lds4<IO>(elem(3, i), x);
+            float z[V], v[V], from[V];
+            lds<IO, V>(elem(q, 0, i), v);
+            if (start) state_of(q, a.s0, o.seq, from);
+            if constexpr (kFrom) {
+              codes_of(q, 2, i, z);
+            } else {
+              if (E && o.first)
+                state_of(q, a.h0, o.seq, z);
+              else
+                lds<IO, V>(elem(q, 2, i), z);
+              if (COMPL) {
+                float x[V];
+                lds<IO, V>(elem(q, 3, i), x);
 #pragma unroll
-              for (int j = 0; j < 4; ++j) z[j] -= x[j];
+                for (int j = 0; j < V; ++j) z[j] -= x[j];
+              }
             }
-          }
+            float dg[V];
 #pragma unroll
-          for (int j = 0; j < 4; ++j) {
-            const float d = v[j] + (start ? from[j] : h[j]);
-            h[j] = al[r][j] * d;
-            dx[j] = COMPL ? u[r][j] * d : d;
-            dg[j] = RAW ? h[j] * z[j] * u[r][j] : h[j] * z[j];
-          }
-          stg4(static_cast<IO*>(a.out) + global_row(i) * a.D + c, dx, n, p.vec);
-          stg4(static_cast<IO*>(a.dg) + global_row(i) * a.D + c, dg, n, p.vec);
-          if (edges.value && q.first && a.sT) {
+            for (int j = 0; j < V / 2; ++j) {
+              const f2 d = add2(pack(v[2 * j], v[2 * j + 1]), start ? pack(from[2 * j], from[2 * j + 1]) : h[j]);
+              h[j] = mul2(al[u][r][j], d);
+              unpack(COMPL ? mul2(in[u][r][j], d) : d, w[2 * j], w[2 * j + 1]);
+              f2 t = mul2(h[j], pack(z[2 * j], z[2 * j + 1]));
+              if (RAW) t = mul2(t, in[u][r][j]);
+              unpack(t, dg[2 * j], dg[2 * j + 1]);
+            }
+            stg<V>(out, w, q.n, p.vec);
+            stg<V>(out2, dg, q.n, p.vec);
 #pragma unroll
-            for (int j = 0; j < 4; ++j)
-              if (j < n) a.sT[(size_t)q.seq * a.D + c + j] = h[j];
+            for (int j = 0; j < V / 2; ++j) unpack(h[j], w[2 * j], w[2 * j + 1]);
+          }
+          if (E && (kDown ? o.first : o.last) && a.sT) {
+#pragma unroll
+            for (int j = 0; j < V; ++j)
+              if (j < q.n) a.sT[(size_t)o.seq * a.D + q.c + j] = w[j];
           }
         }
       }
-      if (kSave && lane < R && t0 + warp * R + lane < a.T) {
-        const ScanCkptLayout l = scan_ckpt_layout(rows, a.D);
-        const size_t at = cb * rows + global_row(warp * R + lane);
-        a.ckpt[l.lam_scale + at] = (uint8_t)lam_code;
-        a.ckpt[l.z_scale + at] = (uint8_t)z_code;
+      if (kSave && lane < kR && q.t0 + warp * kR + lane < a.T) {
+        const size_t at = q.cb * rows + global_row(q, warp * kR + lane);
+        a.ckpt[lay.lam_scale + at] = (uint8_t)lam_code;
+        a.ckpt[lay.z_scale + at] = (uint8_t)z_code;
       }
     };
     if (edge)
@@ -618,7 +826,12 @@ __global__ void __launch_bounds__(256) scan_init_kernel(const TileArgs p, uint4*
   for (size_t i = at; i < count; i += step) words[i] = make_uint4(kEmpty, kEmpty, kEmpty, kEmpty);
   const ScanArgs& a = p.a;
   if (!a.cu) return;
-  for (size_t t = at; t < (size_t)a.T; t += step) {
+  const size_t padded = (size_t)a.T + kInfoPad;  // tiles are read whole
+  for (size_t t = at; t < padded; t += step) {
+    if (t >= (size_t)a.T) {
+      info[t] = -1;
+      continue;
+    }
     int lo = 0, hi = a.N + 1;  // the first of cu[0 .. N] that is past t
     while (lo < hi) {
       const int m = lo + (hi - lo) / 2;
@@ -649,21 +862,22 @@ __global__ void __launch_bounds__(256) scan_step_kernel(const IO* __restrict__ x
   const int n = (int)min((size_t)4, count - i);
   float gv[4], xv[4], s[4];
   if (n == 4) {
-    lds4<IO>(reinterpret_cast<const uint8_t*>(g + i), gv);
-    lds4<IO>(reinterpret_cast<const uint8_t*>(x + i), xv);
+    lds<IO, 4>(reinterpret_cast<const uint8_t*>(g + i), gv);
+    lds<IO, 4>(reinterpret_cast<const uint8_t*>(x + i), xv);
   } else {
 #pragma unroll
     for (int j = 0; j < 4; ++j) gv[j] = j < n ? to_f32(g[i + j]) : 0.f, xv[j] = j < n ? to_f32(x[i + j]) : 0.f;
   }
-  ldg4(state + i, s, n, n == 4);
+  ldg<4>(state + i, s, n, n == 4);
 #pragma unroll
-  for (int j = 0; j < 4; ++j) {
-    float alpha, beta;
-    gate<RAW>(gv[j], alpha, beta);
-    s[j] = fmaf(alpha, s[j], COMPL ? beta * xv[j] : xv[j]);
+  for (int j = 0; j < 4; j += 2) {
+    f2 alpha, beta;
+    gate<RAW>(gv[j], gv[j + 1], alpha, beta);
+    const f2 v = pack(xv[j], xv[j + 1]);
+    unpack(fma2(alpha, pack(s[j], s[j + 1]), COMPL ? mul2(beta, v) : v), s[j], s[j + 1]);
   }
-  stg4(out_state + i, s, n, n == 4);
-  stg4(h + i, s, n, n == 4);
+  stg<4>(out_state + i, s, n, n == 4);
+  stg<4>(h + i, s, n, n == 4);
 }
 
 // ========================================================================= host
@@ -692,8 +906,9 @@ PFN_cuTensorMapEncodeTiled_v12000 encode_fn() {
   return fn;
 }
 
-// [B][T][row of `pitch` elements, `width` of them read]; box 128 channels x `box_rows` rows.
-bool make_map(CUtensorMap* map, const void* base, int eb, int B, int T, size_t width, size_t pitch, int box_rows) {
+// [B][T][row of `pitch` elements, `width` of them read]; box: a tile.
+bool make_map(CUtensorMap* map, const void* base, int eb, int B, int T, size_t width, size_t pitch, int box_width,
+              int box_rows) {
   auto enc = encode_fn();
   if (!enc) return false;
   const CUtensorMapDataType type = eb == 4   ? CU_TENSOR_MAP_DATA_TYPE_FLOAT32
@@ -701,13 +916,14 @@ bool make_map(CUtensorMap* map, const void* base, int eb, int B, int T, size_t w
                                              : CU_TENSOR_MAP_DATA_TYPE_UINT8;
   cuuint64_t dims[3] = {width, (cuuint64_t)T, (cuuint64_t)B};
   cuuint64_t strides[2] = {pitch * eb, pitch * eb * (cuuint64_t)T};
-  cuuint32_t box[3] = {(cuuint32_t)kBlock, (cuuint32_t)box_rows, 1}, es[3] = {1, 1, 1};
+  cuuint32_t box[3] = {(cuuint32_t)box_width, (cuuint32_t)box_rows, 1}, es[3] = {1, 1, 1};
   return enc(map, type, 3, const_cast<void*>(base), dims, strides, box, es, CU_TENSOR_MAP_INTERLEAVE_NONE,
              CU_TENSOR_MAP_SWIZZLE_NONE, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
              CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
-constexpr int kMinRows = kWarps * 4;  // of a tile, over all kinds
+// Whether each chain is walked by one block (no words handed between blocks).
+bool walked(int T, int64_t chains) { return T <= kInOrderRows || chains >= kManyChains; }
 
 int64_t div_up(int64_t a, int64_t b) { return (a + b - 1) / b; }
 size_t align256(size_t v) { return (v + 255) / 256 * 256; }
@@ -736,38 +952,34 @@ cudaError_t launch_tiles(const ScanArgs& a, void* ws, cudaStream_t stream) {
   using S = Shape<K, IO, COMPL>;
   TileArgs p;
   p.a = a;
-  p.blocks = (int)div_up(a.D, kBlock);
+  p.blocks = (int)div_up(a.D, S::W);
   const int64_t chains = (int64_t)a.B * p.blocks, chunks = div_up(a.T, S::kL);
-  p.chains = (int)chains, p.chunks = (int)chunks, p.groups = (int)div_up(chunks, kGroup);
-  p.in_order = a.T <= kInOrderRows;
+  p.chains = (int)chains, p.chunks = (int)chunks;
+  p.groups = (int)div_up(chunks, kGroup);
+  p.in_order = walked(a.T, chains);
   p.vec = a.D % 4 == 0;
   p.tma = (size_t)a.D * sizeof(IO) % 16 == 0;
+  p.words = (size_t)a.D * sizeof(IO) % 4 == 0;
   // workspace: header, pairs, states, row information (the last two kinds of words only where needed)
   uint8_t* w = static_cast<uint8_t*>(ws);
   p.hdr = reinterpret_cast<WorkspaceHeader*>(w);
   w += sizeof(WorkspaceHeader);
   p.pairs = reinterpret_cast<float*>(w);
-  const size_t pair_words = p.in_order ? 0 : (size_t)(chains * chunks) * (2 * kBlock);
-  const size_t state_words = p.in_order ? 0 : (size_t)chains * p.groups * kBlock;
+  const size_t pair_words = p.in_order ? 0 : (size_t)(chains * chunks) * (2 * S::W);
+  const size_t state_words = p.in_order ? 0 : (size_t)chains * p.groups * S::W;
   p.states = p.pairs + pair_words;
   int32_t* info = reinterpret_cast<int32_t*>(p.states + state_words);
   p.info = info;
   if (!ws || (p.in_order && !a.cu)) p.hdr = nullptr;  // no workspace
-  if (p.tma) {
-    const int eb = sizeof(IO);
-    const size_t d = (size_t)a.D;
-    bool ok;
-    if (K == kFwd || K == kFwdCkpt) {
-      ok = make_map(&p.map[0], a.x, eb, a.B, a.T, d, d, S::kL) && make_map(&p.map[1], a.g, eb, a.B, a.T, d, d, S::kL);
-    } else if (K == kBwd) {
-      ok = make_map(&p.map[0], a.dy, eb, a.B, a.T, d, d, S::kL) && make_map(&p.map[1], a.g, eb, a.B, a.T, d, d, S::kL) &&
-           make_map(&p.map[2], a.h, eb, a.B, a.T, d, d, S::kL) &&
-           (!COMPL || make_map(&p.map[3], a.x, eb, a.B, a.T, d, d, S::kL));
-    } else {
+  const void* arrays[4] = {a.x, a.g, nullptr, nullptr};
+  if (S::kDown) arrays[0] = a.dy, arrays[1] = a.g, arrays[2] = a.h, arrays[3] = a.x;
+  for (int i = 0; i < S::kIn; ++i) {
+    bool ok = true;
+    if (K == kBwdCkpt && i > 0) {
       const ScanCkptLayout l = scan_ckpt_layout((size_t)a.B * a.T, a.D);
-      ok = make_map(&p.map[0], a.dy, eb, a.B, a.T, d, d, S::kL) &&
-           make_map(&p.map[1], a.ckpt, 1, a.B, a.T, d, l.pitch, S::kL) &&
-           make_map(&p.map[2], a.ckpt + l.z, 1, a.B, a.T, d, l.pitch, S::kL);
+      ok = make_map(&p.map[i], a.ckpt + (i == 2 ? l.z : 0), 1, a.B, a.T, a.D, l.pitch, S::W, S::kBox);
+    } else if (p.tma) {
+      ok = make_map(&p.map[i], arrays[i], sizeof(IO), a.B, a.T, a.D, a.D, S::W, S::kBox);
     }
     if (!ok) return cudaErrorInvalidValue;
   }
@@ -792,20 +1004,22 @@ cudaError_t launch_tiles(const ScanArgs& a, void* ws, cudaStream_t stream) {
     if (e != cudaSuccess) return e;
   }
   const int64_t grid = p.in_order ? chains : std::min<int64_t>(chains * chunks, (int64_t)sms * S::kPerSm);
-  return launch(kernel, (unsigned)grid, 32 * kWarps, S::kSmem, stream, init, p);
+  return launch(kernel, (unsigned)grid, kThreads, S::kSmem, stream, init, p);
 }
 
 }  // namespace
 
-// Enough for every kind of call: the forward and the backward of a type share one size.
+// Enough for every kind of call of these sizes.
 size_t scan_workspace_bytes(int B, int T, int D, int N, int dtype) {
   (void)dtype;
   if (B == 0 || T == 0) return 0;
-  const int64_t chains = (int64_t)B * div_up(D, kBlock), chunks = div_up(T, kMinRows);
-  size_t bytes = 0;
-  if (T > kInOrderRows)
-    bytes = (size_t)(chains * (2 * chunks + div_up(chunks, kGroup))) * kBlock * sizeof(float);
-  if (N > 0) bytes += align256((size_t)T * 4);
+  size_t words = 0;
+  const auto fit = [&](int width, int rows) {
+    const int64_t chains = (int64_t)B * div_up(D, width), chunks = div_up(T, rows);
+    if (!walked(T, chains)) words = std::max(words, (size_t)(chains * (2 * chunks + div_up(chunks, kGroup)) * width));
+  };
+  fit(16, 28 * kWarps), fit(32, 28 * kWarps), fit(16, 56 * kWarps), fit(128, kR * kWarps);
+  const size_t bytes = words * sizeof(float) + (N > 0 ? align256(((size_t)T + kInfoPad) * 4) : 0);
   return bytes ? sizeof(WorkspaceHeader) + bytes : 0;
 }
 
