@@ -18,11 +18,11 @@
 // the 8-bit checkpoint 8.  So the data is read once, in one pass, in tiles of W
 // channels x L rows, narrow and tall (16 channels, one 32-byte sector of bf16)
 // so that there are many chains of tiles, one per (batch, W channels), and few
-// tiles in each.  A thread folds segments of 7 rows x 2 channels to (A, Bs),
-// alpha and the input staying in its registers; the segments are folded per
-// warp, the warps' pairs by one thread per channel, which also learns what
-// enters the tile; it goes back the same way, and each thread goes over its
-// segments once more.  Tiles of a chain are joined in the order of the rows.
+// tiles in each.  A thread folds a segment of 7 to 15 rows x 2 channels to (A, Bs),
+// alpha and the input staying in its registers; the segments of a warp are
+// folded to one pair, the warps' pairs to the tile's; what enters the tile goes
+// back the same way, and each thread goes over its rows once more.  Results
+// take the inputs' place in shared memory and leave by TMA.  Tiles of a chain are joined in the order of the rows.
 // Many chains (kManyChains), or short ones: a block walks a whole chain, and
 // what leaves a tile stays with it; one barrier per tile.  Few chains: tiles
 // are drawn by ticket in the order of the rows, so whatever a tile waits for
@@ -50,14 +50,26 @@ using namespace sm100;
 constexpr int kBlock = 128;     // channels per scale of the checkpoint
 constexpr int kWarps = 8;
 constexpr int kThreads = 32 * kWarps;
-constexpr int kR = 7;           // rows of a segment: odd, so that the segments of a warp lie in different banks
 constexpr int kGroup = 16;      // few chains: tiles from one published state to the next
 constexpr int kManyChains = 128;   // from so many chains on, each is walked by one block
 constexpr int kInOrderRows = 512;  // and chains of so few rows are, too
 constexpr int kInfoPad = 512;   // rows of padding behind the packed sequences' row information
 constexpr uint32_t kEmpty = 0xffffffffu;     // a word not yet written
-constexpr uint32_t kPollLimit = 1u << 22;    // polls before a wait gives up
-constexpr uint32_t kBarLimit = 1u << 22;
+constexpr uint64_t kGiveUp = 2000000000;     // ns after which a wait gives up
+
+__device__ __forceinline__ uint64_t now_ns() {
+  uint64_t t;
+  asm volatile("mov.u64 %0, %%globaltimer;" : "=l"(t));
+  return t;
+}
+// Waits for a phase of `bar`; false after kGiveUp.
+__device__ __forceinline__ bool wait_for(uint64_t* bar, uint32_t parity) {
+  if (mbar_try_wait(bar, parity)) return true;
+  const uint64_t since = now_ns();
+  while (now_ns() - since < kGiveUp)
+    if (mbar_try_wait(bar, parity)) return true;
+  return false;
+}
 
 // Two floats in one register pair: one instruction for both.
 using f2 = unsigned long long;
@@ -83,6 +95,7 @@ __device__ __forceinline__ f2 fma2(f2 a, f2 b, f2 c) {
   asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
   return r;
 }
+__device__ __forceinline__ f2 neg2(f2 a) { return a ^ 0x8000000080000000ull; }
 __device__ __forceinline__ float ex2_of(float x) {
   float r;
   asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
@@ -118,7 +131,9 @@ __device__ __forceinline__ f2 exp2_of(f2 x) {
 // series where the difference would lose the small rates that make the long
 // memories.
 template <bool RAW>
-__device__ __forceinline__ void gate(float g0, float g1, f2& alpha, f2& beta) {
+__device__ __forceinline__ void gate(f2 g, f2& alpha, f2& beta) {
+  float g0, g1;
+  unpack(g, g0, g1);
   if (RAW) {
     const f2 e = exp2_of(pack(-min_nan(fabsf(g0), 128.f), -min_nan(fabsf(g1), 128.f)));
     float s0, s1, l0, l1;
@@ -160,19 +175,13 @@ __device__ __forceinline__ uint32_t magnitude(float v) {  // for the block's max
   return b < 0x7f800000u ? b : 0u;
 }
 __device__ __forceinline__ bool finite(float v) { return fabsf(v) <= 3.402823466e38f; }
-// Four values as e4m3 of v * inv (inv a power of two; non-finite values give NaN).
-__device__ __forceinline__ uint32_t encode4(const float* v, float inv) {
-  float q[4];
-#pragma unroll
-  for (int j = 0; j < 4; ++j) q[j] = finite(v[j]) ? v[j] * inv : __int_as_float(0x7fffffff);
-  const uint32_t lo = __nv_cvt_float2_to_fp8x2(make_float2(q[0], q[1]), __NV_SATFINITE, __NV_E4M3);
-  const uint32_t hi = __nv_cvt_float2_to_fp8x2(make_float2(q[2], q[3]), __NV_SATFINITE, __NV_E4M3);
-  return lo | hi << 16;
+// Two values as e4m3 of v * inv (inv a power of two; non-finite values give NaN).
+__device__ __forceinline__ uint16_t encode2(const float* v, float inv) {
+  const float a = finite(v[0]) ? v[0] * inv : __int_as_float(0x7fffffff);
+  const float b = finite(v[1]) ? v[1] * inv : __int_as_float(0x7fffffff);
+  return __nv_cvt_float2_to_fp8x2(make_float2(a, b), __NV_SATFINITE, __NV_E4M3);
 }
-__device__ __forceinline__ void decode2(uint16_t c, float scale, float* v) {
-  const float2 x = __half22float2(__half2(__nv_cvt_fp8x2_to_halfraw2(c, __NV_E4M3)));
-  v[0] = x.x * scale, v[1] = x.y * scale;
-}
+__device__ __forceinline__ float2 decode2(uint16_t c) { return __half22float2(__half2(__nv_cvt_fp8x2_to_halfraw2(c, __NV_E4M3))); }
 
 // ----------------------------------------------- V = 2 or 4 channels of a row
 template <typename IO, int V>
@@ -247,6 +256,16 @@ __device__ __forceinline__ void sts(float* p, const float* v) {
   else
     *reinterpret_cast<float2*>(p) = make_float2(v[0], v[1]);
 }
+// Two channels of a result to their place in shared memory.
+template <typename IO>
+__device__ __forceinline__ void put(uint8_t* p, float x, float y) {
+  if constexpr (sizeof(IO) == 4) {
+    *reinterpret_cast<float2*>(p) = make_float2(x, y);
+  } else {
+    const __nv_bfloat162 q = __floats2bfloat162_rn(x, y);
+    *reinterpret_cast<uint32_t*>(p) = *reinterpret_cast<const uint32_t*>(&q);
+  }
+}
 // fp32 or bf16 V channels from anywhere to this thread's place in shared
 // memory, asynchronously where 4-byte pieces are aligned.
 template <typename IO, int V>
@@ -283,43 +302,45 @@ __device__ __forceinline__ uint32_t peek(const float* p) {
 // ------------------------------------------------------------------ the tiles
 enum Kind { kFwd, kFwdCkpt, kBwd, kBwdCkpt };
 
-// Tiles.  A lane holds V channels x U segments.  The forward that writes the
-// checkpoint needs a row's whole scale block in one warp: 128 channels x 56
-// rows, one segment per warp.  The others: 16 channels (32 from the
-// checkpoint, whose codes are one byte), segments side by side in a warp.
-// U and the stages keep two blocks' inputs within an SM's shared memory.
+// Tiles.  A thread holds two channels x one segment of kR rows; kR is odd, so
+// that the segments side by side in a warp lie in different banks, and as
+// large as registers and the stages of two blocks in an SM's shared memory
+// allow.  A unit of a tile is what is folded before the next level: the
+// segments of a warp (16 channels; 32 from the checkpoint, whose codes are one
+// byte), or, in the forward that writes the checkpoint, which needs a row's
+// whole scale block, the one segment of two warps (128 channels); its tile has
+// as many rows as a unit of the forward that does not, so that chains walked
+// in order get the same bits from both.
 template <Kind K, typename IO, bool COMPL>
 struct Shape {
-  static constexpr bool kDown = K == kBwd || K == kBwdCkpt;
-  static constexpr bool kWide = K == kFwdCkpt;
-  static constexpr int V = kWide ? 4 : 2, W = kWide ? 128 : K == kBwdCkpt ? 32 : 16;
-  static constexpr int kAcross = W / V;                     // lanes of a row
-  static constexpr int U = (K == kFwd && sizeof(IO) == 2) || K == kBwdCkpt ? 2 : 1;
-  static constexpr int kSide = 32 / kAcross;                // segments side by side in a warp
-  static constexpr int kSegs = kSide * U;                   // of a warp
-  // Segments folded before the state goes on past them: those of a warp; the
-  // forward that writes the checkpoint keeps to the other's, so that short
-  // sequences, walked in order, get the same bits from both.
-  static constexpr int kFold = !kWide ? kSegs : sizeof(IO) == 2 ? 8 : 4;
-  static constexpr int kWarpRows = kSegs * kR, kL = kWarps * kWarpRows;
-  static constexpr int kBox = kL <= 256 ? kL : kL / 2;      // rows of one TMA copy
+  static constexpr bool kDown = K == kBwd || K == kBwdCkpt, kWide = K == kFwdCkpt;
+  static constexpr int W = kWide ? 128 : K == kBwdCkpt ? 32 : 16;
+  static constexpr int kR = sizeof(IO) == 4 || K == kBwd ? 7 : K == kBwdCkpt ? 13 : 15;
+  static constexpr int kAcross = W / 2;                            // threads of a row
+  static constexpr int kSide = kWide ? 1 : 32 / kAcross;           // segments of a unit
+  static constexpr int kUnits = kWide ? kThreads / kAcross : kWarps;
+  static constexpr int kUnitRows = kSide * kR, kL = kUnits * kUnitRows;
+  static constexpr int kBox = kL <= 256 ? kL : kL / 2;             // rows of one TMA load
   // input arrays: forward x, g; backward dy, g, h, x; from the checkpoint dy, lambda, z
   static constexpr int kIn = K == kBwd ? (COMPL ? 4 : 3) : K == kBwdCkpt ? 3 : 2;
   __host__ __device__ static constexpr int eb(int i) { return K == kBwdCkpt && i > 0 ? 1 : (int)sizeof(IO); }
   __host__ __device__ static constexpr int at(int i) {
     int o = 0;
-    for (int j = 0; j < i; ++j) o += (kL * W * eb(j) + 127) / 128 * 128;
+    for (int j = 0; j < i; ++j) o += kL * W * eb(j);
     return o;
   }
-  static constexpr int kStage = at(kIn);
-  static constexpr int kStages = 3;
-  static constexpr int kSmem = kStages * kStage;
+  static constexpr int kStage = at(kIn), kStages = 3;
+  // the backward's dL/dg takes the place of g, or, for want of it, a buffer of its own behind the stages
+  static constexpr int kOwn = K == kBwdCkpt ? kL * W * (int)sizeof(IO) : 0;
+  static constexpr int kSmem = kStages * kStage + kOwn;
   static constexpr int kPerSm = kSmem > 98304 ? 1 : 2;
+  static_assert(kStage % 128 == 0 && kUnitRows * W * sizeof(IO) % 128 == 0, "TMA needs 128-byte places");
 };
 
 struct TileArgs {
   ScanArgs a;
-  CUtensorMap map[4];
+  CUtensorMap map[4];       // inputs: a tile
+  CUtensorMap out[3];       // h or dL/dx, dL/dg: a unit; with a checkpoint h, lambda and z codes
   WorkspaceHeader* hdr;     // error word; pad[0] is the ticket
   float* pairs;             // [chains][chunks][2][W]
   float* states;            // [chains][groups][W]
@@ -330,15 +351,17 @@ struct TileArgs {
 
 template <typename S>
 struct __align__(128) Shared {
-  float seg[kWarps][S::kSegs][2][S::W];   // (A, Bs) of the segments (wide: in pair)
-  float enter[kWarps][S::kSegs][S::W];    // what enters them
-  float pair[2][kWarps][2][S::W];         // (A, Bs) of the warps, of two tiles (wide: of the segments)
-  float into[kWarps][S::W];               // few chains: what enters them
-  float carry[2][S::W];                   // in order: what leaves a tile
+  float seg[S::kUnits][S::kSide][2][S::W];    // (A, Bs) of the segments, where a unit has several
+  float enter[S::kUnits][S::kSide][S::W];     // what enters them
+  float pair[2][S::kUnits][2][S::W];          // (A, Bs) of the units, of two tiles
+  float into[S::kUnits][S::W];                // few chains: what enters them
+  float carry[2][S::W];                       // in order: what leaves a tile
+  uint32_t top[S::kWide ? kWarps : 1][2][16]; // checkpoint: largest magnitudes of a warp's rows
+  float scale_of[S::kWide ? 1 : kWarps][2][32];  // from the checkpoint: scales of a warp's rows
   uint64_t full[S::kStages];
-  int4 tile[S::kStages];                  // chain, chunk (-1: none left), batch, channel block
-  int info[S::kStages][S::kL];
-  uint8_t scale[S::kStages][2][S::kL + 32];
+  int4 tile[S::kStages];                      // chain, chunk (-1: none left), batch, channel block
+  __align__(16) int info[S::kStages][S::kL];
+  __align__(16) uint8_t scale[S::kStages][2][(S::kL + 47) / 16 * 16];
 };
 
 struct Row {
@@ -350,13 +373,15 @@ template <Kind K, typename IO, bool RAW, bool COMPL>
 __global__ void __launch_bounds__(kThreads, Shape<K, IO, COMPL>::kPerSm)
     scan_tile_kernel(const __grid_constant__ TileArgs p) {
   using S = Shape<K, IO, COMPL>;
-  constexpr int V = S::V, W = S::W, U = S::U, L = S::kL, NS = S::kStages, NSEG = S::kSegs;
+  constexpr int W = S::W, R = S::kR, L = S::kL, NS = S::kStages, NU = S::kUnits;
   constexpr bool kDown = S::kDown, kSave = K == kFwdCkpt, kFrom = K == kBwdCkpt;
   extern __shared__ __align__(128) uint8_t stages[];
   __shared__ Shared<S> sh;
   const ScanArgs& a = p.a;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const int side = lane / S::kAcross, across = lane % S::kAcross;
+  // this thread's unit and segment of it (in the order of the recurrence), and its two channels
+  const int unit = S::kWide ? (int)threadIdx.x / S::kAcross : warp, side = S::kWide ? 0 : lane / S::kAcross;
+  const int across = (int)threadIdx.x % S::kAcross;
   const size_t rows = (size_t)a.B * a.T;
   const bool packed = a.cu != nullptr;
 
@@ -382,7 +407,7 @@ __global__ void __launch_bounds__(kThreads, Shape<K, IO, COMPL>::kPerSm)
     Place q;
     q.chain = tile.x, q.chunk = tile.y, q.b = tile.z, q.cb = tile.w;
     q.t0 = (kDown ? p.chunks - 1 - q.chunk : q.chunk) * (int64_t)L;
-    q.c = q.cb * W + across * V, q.n = a.D - q.c;
+    q.c = q.cb * W + across * 2, q.n = a.D - q.c;
     q.s = k % NS, q.st = stages + q.s * S::kStage;
     return q;
   };
@@ -441,17 +466,17 @@ __global__ void __launch_bounds__(kThreads, Shape<K, IO, COMPL>::kPerSm)
 
   // the k-th tile of this block, chunk -1 past its last
   auto tile_of = [&](int k) {
-    const bool there = mbar_wait(&sh.full[k % NS], (k / NS) & 1, kBarLimit);
+    const bool there = wait_for(&sh.full[k % NS], (k / NS) & 1);
     if (!there) gave_up(202);
     return there ? sh.tile[k % NS] : make_int4(0, -1, 0, 0);
   };
-  // row of the tile: r-th of this lane's u-th segment; segments are numbered in the order of the recurrence
-  auto seg_of = [&](int u) { return u * S::kSide + side; };
-  auto row_at = [&](int u, int r) {
-    const int i = warp * S::kWarpRows + seg_of(u) * kR + r;
+  // the r-th row of this thread's segment, as a row of the tile
+  auto row_at = [&](int r) {
+    const int i = unit * S::kUnitRows + side * R + r;
     return kDown ? L - 1 - i : i;
   };
-  auto elem = [&](const Place& q, int arr, int i) { return q.st + S::at(arr) + (i * W + across * V) * S::eb(arr); };
+  const int lowest = kDown ? L - (unit + 1) * S::kUnitRows : unit * S::kUnitRows;  // row of the unit
+  auto elem = [&](const Place& q, int arr, int i) { return q.st + S::at(arr) + (i * W + across * 2) * S::eb(arr); };
   auto global_row = [&](const Place& q, int i) { return (size_t)q.b * a.T + q.t0 + i; };
   auto row_info = [&](const Place& q, int i) {
     Row o;
@@ -464,48 +489,47 @@ __global__ void __launch_bounds__(kThreads, Shape<K, IO, COMPL>::kPerSm)
     }
     return o;
   };
-  // whether any of the warp's rows starts or ends a sequence or belongs to none
+  // whether any of the unit's rows starts or ends a sequence or belongs to none
   auto has_edge = [&](const Place& q) {
-    const int lo = kDown ? L - (warp + 1) * S::kWarpRows : warp * S::kWarpRows;
-    if (!packed) return q.t0 + lo == 0 || q.t0 + lo + S::kWarpRows >= a.T;
+    if (!packed) return q.t0 + lowest == 0 || q.t0 + lowest + S::kUnitRows >= a.T;
     bool edge = false;
-    for (int i = lane; i < S::kWarpRows; i += 32) {
-      const int v = sh.info[q.s][lo + i];
+    for (int i = lane; i < S::kUnitRows; i += 32) {
+      const int v = sh.info[q.s][lowest + i];
       edge |= v < 0 || (v & 3);
     }
     return __any_sync(0xffffffffu, edge) != 0;
   };
-  auto state_of = [&](const Place& q, const float* base, int seq, float* v) {
-    ldg<V>(base ? base + (size_t)seq * a.D + q.c : nullptr, v, q.n, p.vec);
+  auto state_of = [&](const Place& q, const float* base, int seq) {
+    float v[2];
+    ldg<2>(base ? base + (size_t)seq * a.D + q.c : nullptr, v, q.n, p.vec);
+    return pack(v[0], v[1]);
   };
-  auto codes_of = [&](const Place& q, int arr, int i, float* v) {
-    decode2(*reinterpret_cast<const uint16_t*>(elem(q, arr, i)), pow2(sh.scale[q.s][arr - 1][(scale_at(q) & 15) + i]), v);
+  auto load2 = [&](const Place& q, int arr, int i) {
+    float v[2];
+    lds<IO, 2>(elem(q, arr, i), v);
+    return pack(v[0], v[1]);
   };
-  auto load_gate = [&](const Place& q, int i, float* g) {
-    if constexpr (kFrom)
-      codes_of(q, 1, i, g);
-    else
-      lds<IO, V>(elem(q, 1, i), g);
+  auto codes_of = [&](const Place& q, int arr, int i) {
+    const float2 x = decode2(*reinterpret_cast<const uint16_t*>(elem(q, arr, i)));
+    return mul2(pack(x.x, x.y), both(sh.scale_of[warp][arr - 1][i - lowest]));
   };
-  // rows that TMA cannot take (their pitch is no multiple of 16 bytes): each lane brings its own channels of tile k
+  // rows that TMA cannot take (their pitch is no multiple of 16 bytes): each thread brings its own channels of tile k
   auto bring_tile = [&](int k) {
     const int4 tile = tile_of(k);
     if (tile.y >= 0) {
       const Place q = place_of(k, tile);
+      for (int r = 0; r < R; ++r) {
+        const int i = row_at(r);
+        const bool in = q.t0 + i < a.T && q.n > 0;
 #pragma unroll
-      for (int u = 0; u < U; ++u)
-        for (int r = 0; r < kR; ++r) {
-          const int i = row_at(u, r);
-          const bool in = q.t0 + i < a.T && q.n > 0;
-#pragma unroll
-          for (int arr = 0; arr < (kFrom ? 1 : S::kIn); ++arr) {
-            const void* src = !kDown ? (arr == 0 ? a.x : a.g) : (arr == 0 ? a.dy : arr == 1 ? a.g : arr == 2 ? a.h : a.x);
-            const bool up = K == kBwd && arr == 2;
-            const bool ok = in && (!up || q.t0 + i > 0);
-            bring<IO, V>(elem(q, arr, i), static_cast<const IO*>(src) + (ok ? (global_row(q, i) - up) * a.D + q.c : 0),
-                         ok ? q.n : 0, p.words);
-          }
+        for (int arr = 0; arr < (kFrom ? 1 : S::kIn); ++arr) {
+          const void* src = !kDown ? (arr == 0 ? a.x : a.g) : (arr == 0 ? a.dy : arr == 1 ? a.g : arr == 2 ? a.h : a.x);
+          const bool up = K == kBwd && arr == 2;
+          const bool ok = in && (!up || q.t0 + i > 0);
+          bring<IO, 2>(elem(q, arr, i), static_cast<const IO*>(src) + (ok ? (global_row(q, i) - up) * a.D + q.c : 0),
+                       ok ? q.n : 0, p.words);
         }
+      }
     }
     asm volatile("cp.async.commit_group;" ::: "memory");
   };
@@ -520,65 +544,61 @@ __global__ void __launch_bounds__(kThreads, Shape<K, IO, COMPL>::kPerSm)
       asm volatile("cp.async.wait_group 1;" ::: "memory");
     }
     const Place q = place_of(k, tile);
-    const bool edge = has_edge(q);
+    // rows out of the ordinary: none in most tiles
+    const bool edge = has_edge(q) || !p.tma;
     float(*pair)[2][W] = sh.pair[k & 1];
+    if constexpr (kFrom) {
+      if (lane < S::kUnitRows) {
+        const int off = (int)(scale_at(q) & 15) + lowest + lane;
+        sh.scale_of[warp][0][lane] = pow2(sh.scale[q.s][0][off]);
+        sh.scale_of[warp][1][lane] = pow2(sh.scale[q.s][1][off]);
+      }
+      __syncwarp();
+    }
 
     // ---- segments as pairs
-    f2 al[U][kR][V / 2], in[U][kR][V / 2];  // alpha; forward: the input, backward: 1 - alpha
+    f2 al[R], in[R];  // alpha; forward: the input, backward: 1 - alpha
     auto reduce = [&](auto edges) {
       constexpr bool E = decltype(edges)::value;
+      f2 A = both(1.f), B = both(0.f);
 #pragma unroll
-      for (int u = 0; u < U; ++u) {
-        f2 A[V / 2], B[V / 2];
-#pragma unroll
-        for (int j = 0; j < V / 2; ++j) A[j] = both(1.f), B[j] = both(0.f);
-#pragma unroll
-        for (int r = 0; r < kR; ++r) {
-          const int i = row_at(u, r);
-          float g[V], v[V], from[V];
-          load_gate(q, i, g);
-          lds<IO, V>(elem(q, 0, i), v);
-          const Row o = E ? row_info(q, i) : Row{true, false, false, 0};
-          const bool start = E && o.valid && (kDown ? o.last : o.first);
-          if (start) state_of(q, a.s0, o.seq, from);
-#pragma unroll
-          for (int j = 0; j < V / 2; ++j) {
-            f2 be;
-            gate<RAW && !kFrom>(g[2 * j], g[2 * j + 1], al[u][r][j], be);
-            const f2 x = pack(v[2 * j], v[2 * j + 1]);
-            in[u][r][j] = kDown ? be : COMPL ? mul2(be, x) : x;
-            if (E && !o.valid) continue;
-            if (start) {
-              const f2 f = pack(from[2 * j], from[2 * j + 1]);
-              if (!kDown) in[u][r][j] = fma2(al[u][r][j], f, in[u][r][j]);
-              A[j] = both(-0.f);
-              B[j] = kDown ? mul2(al[u][r][j], add2(x, f)) : in[u][r][j];
-            } else {
-              A[j] = mul2(A[j], al[u][r][j]);
-              B[j] = kDown ? mul2(al[u][r][j], add2(B[j], x)) : fma2(al[u][r][j], B[j], in[u][r][j]);
-            }
-          }
+      for (int r = 0; r < R; ++r) {
+        const int i = row_at(r);
+        f2 g, be;
+        if constexpr (kFrom) g = codes_of(q, 1, i);
+        else g = load2(q, 1, i);
+        const f2 x = load2(q, 0, i);
+        gate<RAW && !kFrom>(g, al[r], be);
+        in[r] = kDown ? be : COMPL ? mul2(be, x) : x;
+        const Row o = E ? row_info(q, i) : Row{true, false, false, 0};
+        if (E && !o.valid) continue;
+        if (E && (kDown ? o.last : o.first)) {
+          const f2 f = state_of(q, a.s0, o.seq);
+          if (!kDown) in[r] = fma2(al[r], f, in[r]);
+          A = both(-0.f);
+          B = kDown ? mul2(al[r], add2(x, f)) : in[r];
+        } else {
+          A = mul2(A, al[r]);
+          B = kDown ? mul2(al[r], add2(B, x)) : fma2(al[r], B, in[r]);
         }
-        float(*to)[W] = S::kWide ? pair[warp] : sh.seg[warp][seg_of(u)];
-        float f[V];
-#pragma unroll
-        for (int j = 0; j < V / 2; ++j) unpack(A[j], f[2 * j], f[2 * j + 1]);
-        sts<V>(&to[0][across * V], f);
-#pragma unroll
-        for (int j = 0; j < V / 2; ++j) unpack(B[j], f[2 * j], f[2 * j + 1]);
-        sts<V>(&to[1][across * V], f);
       }
+      float(*to)[W] = S::kSide == 1 ? pair[unit] : sh.seg[unit][side];
+      float f[2];
+      unpack(A, f[0], f[1]);
+      sts<2>(&to[0][across * 2], f);
+      unpack(B, f[0], f[1]);
+      sts<2>(&to[1][across * 2], f);
     };
     if (edge)
       reduce(std::true_type{});
     else
       reduce(std::false_type{});
-    if constexpr (!S::kWide) {  // the warp's pair
+    if constexpr (S::kSide > 1) {  // the unit's pair
       __syncwarp();
       if (lane < W) {
         float ta = sh.seg[warp][0][0][lane], tb = sh.seg[warp][0][1][lane];
 #pragma unroll
-        for (int g = 1; g < NSEG; ++g) {
+        for (int g = 1; g < S::kSide; ++g) {
           const float wa = sh.seg[warp][g][0][lane], wb = sh.seg[warp][g][1][lane];
           tb = through(tb, wa, wb);
           ta = fresh(wa) ? wa : ta * wa;
@@ -586,10 +606,11 @@ __global__ void __launch_bounds__(kThreads, Shape<K, IO, COMPL>::kPerSm)
         pair[warp][0][lane] = ta, pair[warp][1][lane] = tb;
       }
     }
+    if (lane == 0) bulk_wait_read();  // the tile before has left its stage
     __syncthreads();  // the pairs are there, and every warp is done with the tile before
     if (threadIdx.x == 0) feed(k + 2);  // into its stage
 
-    // ---- what enters the warps, from what enters the tile: one thread per channel
+    // ---- few chains: what enters the units, one thread per channel
     if (!p.in_order) {
       const int place = q.chunk % kGroup;
       if (warp < (W + 31) / 32) {  // with 16 channels both halves of the warp do the same
@@ -597,13 +618,14 @@ __global__ void __launch_bounds__(kThreads, Shape<K, IO, COMPL>::kPerSm)
         float* state = p.states + ((size_t)q.chain * p.groups + q.chunk / kGroup) * W + ch;
         float* pairs = p.pairs + ((size_t)q.chain * p.chunks + q.chunk) * (2 * W) + ch;
         auto arrived = [&](const float* at, uint32_t v) {
-          for (uint32_t i = 0; v == kEmpty; ++i) {
-            if (i >= (failed ? 1u : kPollLimit)) {
-              failed = true;
-              gave_up(203);
-              break;
-            }
-            v = peek(at);
+          if (v == kEmpty && !failed) {
+            const uint64_t since = now_ns();
+            while ((v = peek(at)) == kEmpty)
+              if (now_ns() - since > kGiveUp) {
+                failed = true;
+                gave_up(203);
+                break;
+              }
           }
           return __uint_as_float(v);
         };
@@ -611,7 +633,7 @@ __global__ void __launch_bounds__(kThreads, Shape<K, IO, COMPL>::kPerSm)
         if (q.chunk >= kGroup) head = peek(state - W);
         float ta = pair[0][0][ch], tb = pair[0][1][ch];
 #pragma unroll
-        for (int w = 1; w < kWarps; ++w) {
+        for (int w = 1; w < NU; ++w) {
           const float wa = pair[w][0][ch], wb = pair[w][1][ch];
           tb = through(tb, wa, wb);
           ta = fresh(wa) ? wa : ta * wa;
@@ -637,182 +659,178 @@ __global__ void __launch_bounds__(kThreads, Shape<K, IO, COMPL>::kPerSm)
         h = through(h, ga, gb);
         if (place == kGroup - 1) publish(state, through(h, ta, tb));
 #pragma unroll
-        for (int w = 0; w < kWarps; ++w) {
+        for (int w = 0; w < NU; ++w) {
           sh.into[w][ch] = h;
           h = through(h, pair[w][0][ch], pair[w][1][ch]);
         }
       }
       __syncthreads();
     }
-    if constexpr (S::kWide) {
+
+    // ---- what enters this thread's segment
+    f2 h;  // forward: the state, backward: c_{t+1}
+    {
+      constexpr int kMine = S::kWide ? 2 : 1;  // channels of a thread on this way
+      if (S::kWide || lane < W) {
+        const int ch = S::kWide ? across * 2 : lane;
+        float e[2];
 #pragma unroll
-      for (int j = 0; j < V; ++j) {
-        const int ch = lane * V + j;
-        float h;
-        if (!p.in_order) {
-          h = sh.into[warp][ch];
-        } else {
-          // carry through the earlier folds of the tile, then segment by segment
-          h = k > 0 ? sh.carry[k & 1][ch] : 0.f;
-          float fa = 1.f, fb = 0.f;
-          for (int w = 0; w < kWarps; ++w) {
-            if (w >= warp && warp != kWarps - 1) break;
-            const float wa = pair[w][0][ch], wb = pair[w][1][ch];
-            fb = w % S::kFold == 0 ? wb : through(fb, wa, wb);
-            fa = w % S::kFold == 0 || fresh(wa) ? wa : fa * wa;
-            if (w % S::kFold == S::kFold - 1) {
-              if (w < warp) h = through(h, fa, fb);
-              else sh.carry[(k + 1) & 1][ch] = through(h, fa, fb);
+        for (int j = 0; j < kMine; ++j) {
+          if (!p.in_order) {
+            e[j] = sh.into[unit][ch + j];
+          } else {
+            e[j] = k > 0 ? sh.carry[k & 1][ch + j] : 0.f;
+            if constexpr (S::kWide) {  // the tile is one unit of the other forward: its carry goes through the whole
+              if (unit == NU - 1) {
+                float fa = pair[0][0][ch + j], fb = pair[0][1][ch + j];
+#pragma unroll
+                for (int w = 1; w < NU; ++w) {
+                  const float wa = pair[w][0][ch + j], wb = pair[w][1][ch + j];
+                  fb = through(fb, wa, wb);
+                  fa = fresh(wa) ? wa : fa * wa;
+                }
+                sh.carry[(k + 1) & 1][ch + j] = through(e[j], fa, fb);
+              }
             }
+            for (int w = 0; w < unit; ++w) e[j] = through(e[j], pair[w][0][ch + j], pair[w][1][ch + j]);
+            if (!S::kWide && unit == NU - 1)
+              sh.carry[(k + 1) & 1][ch + j] = through(e[j], pair[unit][0][ch + j], pair[unit][1][ch + j]);
           }
-          for (int w = warp / S::kFold * S::kFold; w < warp; ++w) h = through(h, pair[w][0][ch], pair[w][1][ch]);
         }
-        sh.enter[warp][0][ch] = h;
-      }
-    } else if (lane < W) {
-      float h;
-      if (!p.in_order) {
-        h = sh.into[warp][lane];
-      } else {
-        h = k > 0 ? sh.carry[k & 1][lane] : 0.f;
-        for (int w = 0; w < warp; ++w) h = through(h, pair[w][0][lane], pair[w][1][lane]);
-        if (warp == kWarps - 1) sh.carry[(k + 1) & 1][lane] = through(h, pair[warp][0][lane], pair[warp][1][lane]);
-      }
+        if constexpr (S::kWide) {
+          h = pack(e[0], e[1]);
+        } else {
 #pragma unroll
-      for (int g = 0; g < NSEG; ++g) {
-        sh.enter[warp][g][lane] = h;
-        h = through(h, sh.seg[warp][g][0][lane], sh.seg[warp][g][1][lane]);
+          for (int g = 0; g < S::kSide; ++g) {
+            sh.enter[warp][g][lane] = e[0];
+            e[0] = through(e[0], sh.seg[warp][g][0][lane], sh.seg[warp][g][1][lane]);
+          }
+        }
+      }
+      if constexpr (!S::kWide) {
+        __syncwarp();
+        const float2 e = *reinterpret_cast<const float2*>(&sh.enter[warp][side][across * 2]);
+        h = pack(e.x, e.y);
       }
     }
-    __syncwarp();
 
-    // ---- the rows themselves
-    const int64_t step = kDown ? -(int64_t)a.D : (int64_t)a.D;
+    // ---- the rows themselves, results into the stage
+    // dL/dg: its place
+    auto second = [&](int i) {
+      return kFrom ? stages + NS * S::kStage + (i * W + across * 2) * sizeof(IO) : elem(q, 1, i);
+    };
+    auto store = [&](IO* base, uint8_t* place, int i, f2 v, bool direct) {
+      float w[2];
+      unpack(v, w[0], w[1]);
+      if (direct)
+        stg<2>(base + global_row(q, i) * a.D + q.c, w, q.n, p.vec);
+      else
+        put<IO>(place, w[0], w[1]);
+    };
     auto emit = [&](auto edges) {
       constexpr bool E = decltype(edges)::value;
-      int lam_code = 0, z_code = 0;  // of the warp's row `lane`
+      const bool direct = E && !p.tma;
 #pragma unroll
-      for (int u = 0; u < U; ++u) {
-        f2 h[V / 2];  // the state that enters (forward), c_{t+1} (backward)
-        {
-          float f[V];
-          lds<float, V>(reinterpret_cast<const uint8_t*>(&sh.enter[warp][seg_of(u)][across * V]), f);
-#pragma unroll
-          for (int j = 0; j < V / 2; ++j) h[j] = pack(f[2 * j], f[2 * j + 1]);
+      for (int r = 0; r < R; ++r) {
+        const int i = row_at(r);
+        const Row o = E ? row_info(q, i) : Row{true, false, false, 0};
+        if (E && !o.valid) {  // past the end, or a row that no sequence owns
+          al[r] = in[r] = both(0.f);
+          if (!direct || q.t0 + i < a.T) {
+            store(static_cast<IO*>(a.out), elem(q, 0, i), i, both(0.f), direct);
+            if (kDown) store(static_cast<IO*>(a.dg), second(i), i, both(0.f), direct);
+          }
+          continue;
         }
-        const size_t from_row = global_row(q, row_at(u, 0));
-        IO* out = static_cast<IO*>(a.out) + from_row * a.D + q.c;
-        IO* out2 = static_cast<IO*>(a.dg) + (kDown ? from_row * a.D + q.c : 0);
-#pragma unroll
-        for (int r = 0; r < kR; ++r, out += step, out2 += step) {
-          const int i = row_at(u, r);
-          const Row o = E ? row_info(q, i) : Row{true, false, false, 0};
-          if (E && !o.valid) {
-            if (packed && q.t0 + i < a.T) {  // a row that no sequence owns
-              float zero[V];
-#pragma unroll
-              for (int j = 0; j < V; ++j) zero[j] = 0.f;
-              stg<V>(out, zero, q.n, p.vec);
-              if (kDown) stg<V>(out2, zero, q.n, p.vec);
-              if (kSave) {
-                if (q.n > 0) {
-                  *reinterpret_cast<uint32_t*>(a.ckpt + global_row(q, i) * lay.pitch + q.c) = 0;
-                  *reinterpret_cast<uint32_t*>(a.ckpt + lay.z + global_row(q, i) * lay.pitch + q.c) = 0;
-                }
-                if (lane == r) lam_code = z_code = 1;
-              }
+        const bool start = E && (kDown ? o.last : o.first);
+        if constexpr (!kDown) {
+          [[maybe_unused]] f2 z, lam;
+          if constexpr (kSave) {
+            z = start ? state_of(q, a.s0, o.seq) : h;
+            if (COMPL) z = add2(z, neg2(load2(q, 0, i)));
+            lam = load2(q, 1, i);
+            if (RAW) {
+              float l0, l1;
+              unpack(lam, l0, l1);
+              lam = pack(q.n > 0 ? log_sigmoid(l0) : 0.f, q.n > 1 ? log_sigmoid(l1) : 0.f);
             }
-            continue;
           }
-          const bool start = E && (kDown ? o.last : o.first);
-          float w[V];  // what is stored
-          if constexpr (!kDown) {
-            [[maybe_unused]] float z[V], lam[V];
-            if constexpr (kSave) {
-              float g[V], x[V];
-              load_gate(q, i, g);
-              if (start)
-                state_of(q, a.s0, o.seq, z);
-              else
-#pragma unroll
-                for (int j = 0; j < V / 2; ++j) unpack(h[j], z[2 * j], z[2 * j + 1]);
-              if (COMPL) {
-                lds<IO, V>(elem(q, 0, i), x);
-#pragma unroll
-                for (int j = 0; j < V; ++j) z[j] -= x[j];
-              }
-#pragma unroll
-              for (int j = 0; j < V; ++j) lam[j] = !RAW ? g[j] : j < q.n ? log_sigmoid(g[j]) : 0.f;
-            }
-#pragma unroll
-            for (int j = 0; j < V / 2; ++j) {
-              h[j] = start ? in[u][r][j] : fma2(al[u][r][j], h[j], in[u][r][j]);
-              unpack(h[j], w[2 * j], w[2 * j + 1]);
-            }
-            stg<V>(out, w, q.n, p.vec);
-            if constexpr (kSave) {
-              uint32_t ml = 0, mz = 0;
-#pragma unroll
-              for (int j = 0; j < V; ++j) ml = max(ml, magnitude(lam[j])), mz = max(mz, magnitude(z[j]));
-              const int kl = scale_code(__uint_as_float(__reduce_max_sync(0xffffffffu, ml)));
-              const int kz = scale_code(__uint_as_float(__reduce_max_sync(0xffffffffu, mz)));
-              if (q.n > 0) {
-                *reinterpret_cast<uint32_t*>(a.ckpt + global_row(q, i) * lay.pitch + q.c) = encode4(lam, pow2(254 - kl));
-                *reinterpret_cast<uint32_t*>(a.ckpt + lay.z + global_row(q, i) * lay.pitch + q.c) = encode4(z, pow2(254 - kz));
-              }
-              if (lane == r) lam_code = kl, z_code = kz;
-            }
-          } else {
-            float z[V], v[V], from[V];
-            lds<IO, V>(elem(q, 0, i), v);
-            if (start) state_of(q, a.s0, o.seq, from);
-            if constexpr (kFrom) {
-              codes_of(q, 2, i, z);
-            } else {
-              if (E && o.first)
-                state_of(q, a.h0, o.seq, z);
-              else
-                lds<IO, V>(elem(q, 2, i), z);
-              if (COMPL) {
-                float x[V];
-                lds<IO, V>(elem(q, 3, i), x);
-#pragma unroll
-                for (int j = 0; j < V; ++j) z[j] -= x[j];
-              }
-            }
-            float dg[V];
-#pragma unroll
-            for (int j = 0; j < V / 2; ++j) {
-              const f2 d = add2(pack(v[2 * j], v[2 * j + 1]), start ? pack(from[2 * j], from[2 * j + 1]) : h[j]);
-              h[j] = mul2(al[u][r][j], d);
-              unpack(COMPL ? mul2(in[u][r][j], d) : d, w[2 * j], w[2 * j + 1]);
-              f2 t = mul2(h[j], pack(z[2 * j], z[2 * j + 1]));
-              if (RAW) t = mul2(t, in[u][r][j]);
-              unpack(t, dg[2 * j], dg[2 * j + 1]);
-            }
-            stg<V>(out, w, q.n, p.vec);
-            stg<V>(out2, dg, q.n, p.vec);
-#pragma unroll
-            for (int j = 0; j < V / 2; ++j) unpack(h[j], w[2 * j], w[2 * j + 1]);
+          h = start ? in[r] : fma2(al[r], h, in[r]);
+          store(static_cast<IO*>(a.out), elem(q, 0, i), i, h, direct);
+          if constexpr (kSave) al[r] = lam, in[r] = z;
+        } else {
+          f2 z;
+          if constexpr (kFrom) z = codes_of(q, 2, i);
+          else {
+            z = E && o.first ? state_of(q, a.h0, o.seq) : load2(q, 2, i);
+            if (COMPL) z = add2(z, neg2(load2(q, 3, i)));
           }
-          if (E && (kDown ? o.first : o.last) && a.sT) {
-#pragma unroll
-            for (int j = 0; j < V; ++j)
-              if (j < q.n) a.sT[(size_t)o.seq * a.D + q.c + j] = w[j];
-          }
+          const f2 d = add2(load2(q, 0, i), start ? state_of(q, a.s0, o.seq) : h);
+          h = mul2(al[r], d);
+          f2 dg = mul2(h, z);
+          if (RAW) dg = mul2(dg, in[r]);
+          store(static_cast<IO*>(a.out), elem(q, 0, i), i, COMPL ? mul2(in[r], d) : d, direct);
+          store(static_cast<IO*>(a.dg), second(i), i, dg, direct);
         }
-      }
-      if (kSave && lane < kR && q.t0 + warp * kR + lane < a.T) {
-        const size_t at = q.cb * rows + global_row(q, warp * kR + lane);
-        a.ckpt[lay.lam_scale + at] = (uint8_t)lam_code;
-        a.ckpt[lay.z_scale + at] = (uint8_t)z_code;
+        if (E && (kDown ? o.first : o.last) && a.sT) {
+          float w[2];
+          unpack(h, w[0], w[1]);
+#pragma unroll
+          for (int j = 0; j < 2; ++j)
+            if (j < q.n) a.sT[(size_t)o.seq * a.D + q.c + j] = w[j];
+        }
       }
     };
     if (edge)
       emit(std::true_type{});
     else
       emit(std::false_type{});
+
+    if constexpr (kSave) {
+      // ---- al and in hold lambda and z now: the rows' scales, then the codes into g's place, unit by unit
+      float v[2];
+#pragma unroll
+      for (int r = 0; r < R; ++r) {
+#pragma unroll
+        for (int m = 0; m < 2; ++m) {
+          unpack(m ? in[r] : al[r], v[0], v[1]);
+          const uint32_t top = __reduce_max_sync(0xffffffffu, max(magnitude(v[0]), magnitude(v[1])));
+          if (lane == 0) sh.top[warp][m][r] = top;
+        }
+      }
+      named_bar_sync(1 + unit, S::kAcross);
+      uint8_t* codes = q.st + S::at(1) + unit * S::kUnitRows * W * (int)sizeof(IO);
+#pragma unroll
+      for (int r = 0; r < R; ++r) {
+#pragma unroll
+        for (int m = 0; m < 2; ++m) {
+          const int code = scale_code(__uint_as_float(max(sh.top[warp][m][r], sh.top[warp ^ 1][m][r])));
+          unpack(m ? in[r] : al[r], v[0], v[1]);
+          *reinterpret_cast<uint16_t*>(codes + (m * R + r) * W + across * 2) = encode2(v, pow2(254 - code));
+          if (across == r && q.t0 + row_at(r) < a.T)
+            a.ckpt[(m ? lay.z_scale : lay.lam_scale) + q.cb * rows + global_row(q, row_at(r))] = (uint8_t)code;
+        }
+      }
+    }
+    // ---- out by TMA, each unit's rows (rows past T are not written)
+    fence_async_smem();
+    if constexpr (S::kWide)
+      named_bar_sync(1 + unit, S::kAcross);
+    else
+      __syncwarp();
+    if ((S::kWide ? across == 0 : lane == 0) && q.t0 + lowest < a.T) {
+      const int c0 = q.cb * W, t = (int)q.t0 + lowest;
+      const auto leave = [&](const CUtensorMap& map, const uint8_t* from) { tma_store_3d(&map, from, c0, t, q.b); };
+      const int at = lowest * W * (int)sizeof(IO);
+      if (p.tma) {
+        leave(p.out[0], q.st + at);
+        if (kDown) leave(p.out[1], (kFrom ? stages + NS * S::kStage : q.st + S::at(1)) + at);
+      }
+      if (kSave) leave(p.out[1], q.st + S::at(1) + at), leave(p.out[2], q.st + S::at(1) + at + R * W);
+      bulk_commit();
+    }
   }
+  if (lane == 0) bulk_wait_read();
 }
 
 // Before a sequence call: header and ticket cleared, the words that blocks
@@ -872,7 +890,7 @@ __global__ void __launch_bounds__(256) scan_step_kernel(const IO* __restrict__ x
 #pragma unroll
   for (int j = 0; j < 4; j += 2) {
     f2 alpha, beta;
-    gate<RAW>(gv[j], gv[j + 1], alpha, beta);
+    gate<RAW>(pack(gv[j], gv[j + 1]), alpha, beta);
     const f2 v = pack(xv[j], xv[j + 1]);
     unpack(fma2(alpha, pack(s[j], s[j + 1]), COMPL ? mul2(beta, v) : v), s[j], s[j + 1]);
   }
@@ -973,16 +991,20 @@ cudaError_t launch_tiles(const ScanArgs& a, void* ws, cudaStream_t stream) {
   if (!ws || (p.in_order && !a.cu)) p.hdr = nullptr;  // no workspace
   const void* arrays[4] = {a.x, a.g, nullptr, nullptr};
   if (S::kDown) arrays[0] = a.dy, arrays[1] = a.g, arrays[2] = a.h, arrays[3] = a.x;
+  const ScanCkptLayout l = scan_ckpt_layout((size_t)a.B * a.T, a.D);
+  bool ok = true;
   for (int i = 0; i < S::kIn; ++i) {
-    bool ok = true;
-    if (K == kBwdCkpt && i > 0) {
-      const ScanCkptLayout l = scan_ckpt_layout((size_t)a.B * a.T, a.D);
-      ok = make_map(&p.map[i], a.ckpt + (i == 2 ? l.z : 0), 1, a.B, a.T, a.D, l.pitch, S::W, S::kBox);
-    } else if (p.tma) {
-      ok = make_map(&p.map[i], arrays[i], sizeof(IO), a.B, a.T, a.D, a.D, S::W, S::kBox);
-    }
-    if (!ok) return cudaErrorInvalidValue;
+    if (K == kBwdCkpt && i > 0)
+      ok = ok && make_map(&p.map[i], a.ckpt + (i == 2 ? l.z : 0), 1, a.B, a.T, a.D, l.pitch, S::W, S::kBox);
+    else if (p.tma)
+      ok = ok && make_map(&p.map[i], arrays[i], sizeof(IO), a.B, a.T, a.D, a.D, S::W, S::kBox);
   }
+  if (p.tma) ok = ok && make_map(&p.out[0], a.out, sizeof(IO), a.B, a.T, a.D, a.D, S::W, S::kUnitRows);
+  if (p.tma && S::kDown) ok = ok && make_map(&p.out[1], a.dg, sizeof(IO), a.B, a.T, a.D, a.D, S::W, S::kUnitRows);
+  if (K == kFwdCkpt)
+    for (int i = 1; i <= 2; ++i)
+      ok = ok && make_map(&p.out[i], a.ckpt + (i == 2 ? l.z : 0), 1, a.B, a.T, a.D, l.pitch, S::W, S::kUnitRows);
+  if (!ok) return cudaErrorInvalidValue;
   auto kernel = scan_tile_kernel<K, IO, RAW, COMPL>;
   static std::atomic<uint64_t> ready{0};  // devices whose shared-memory limit has been raised
   int dev = 0;
@@ -1018,7 +1040,7 @@ size_t scan_workspace_bytes(int B, int T, int D, int N, int dtype) {
     const int64_t chains = (int64_t)B * div_up(D, width), chunks = div_up(T, rows);
     if (!walked(T, chains)) words = std::max(words, (size_t)(chains * (2 * chunks + div_up(chunks, kGroup)) * width));
   };
-  fit(16, 28 * kWarps), fit(32, 28 * kWarps), fit(16, 56 * kWarps), fit(128, kR * kWarps);
+  fit(16, 28 * kWarps), fit(16, 60 * kWarps), fit(32, 26 * kWarps), fit(32, 14 * kWarps), fit(128, 28), fit(128, 60);
   const size_t bytes = words * sizeof(float) + (N > 0 ? align256(((size_t)T + kInfoPad) * 4) : 0);
   return bytes ? sizeof(WorkspaceHeader) + bytes : 0;
 }
