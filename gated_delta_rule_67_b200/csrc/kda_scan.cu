@@ -16,23 +16,32 @@
 //
 // What bounds it: bytes.  bf16 forward 6 B per element, backward 10-12, from
 // the 8-bit checkpoint 8.  So the data is read once, in one pass, in tiles of W
-// channels x L rows, narrow and tall (16 channels, one 32-byte sector of bf16)
-// so that there are many chains of tiles, one per (batch, W channels), and few
-// tiles in each.  A thread folds a segment of 7 to 15 rows x 2 channels to (A, Bs),
-// alpha and the input staying in its registers; the segments of a warp are
-// folded to one pair, the warps' pairs to the tile's; what enters the tile goes
-// back the same way, and each thread goes over its rows once more.  Results
-// take the inputs' place in shared memory and leave by TMA.  Tiles of a chain are joined in the order of the rows.
-// Many chains (kManyChains), or short ones: a block walks a whole chain, and
-// what leaves a tile stays with it; one barrier per tile.  Few chains: tiles
-// are drawn by ticket in the order of the rows, so whatever a tile waits for
-// belongs to a block that is running; each tile publishes its (A, Bs), the
-// last of every kGroup tiles the state that leaves them, and a tile folds the
-// pairs of the earlier ones of its group onto the state that left the group
-// before; the words handed on are their own flags (all bits set = not yet
-// written), so one trip to L2 sees and fetches them.  The order of the fold
-// depends on the sizes alone, so the bits are the same every time.
-// The tile after next is on its way (TMA, three stages) while one is computed.
+// channels x L rows, as narrow as memory allows (rows of 64 bytes; of 32 they
+// come at two thirds of the rate) so that there are many chains of tiles, one
+// per (batch, W channels), and few tiles in each.  A thread folds a segment of
+// 7 to 15 rows x 2 channels to (A, Bs), alpha and the input staying in its
+// registers; the segments of a warp (a unit) are folded to one pair, the
+// units' pairs to the tile's; what enters the tile goes back the same way, and
+// each thread goes over its rows once more.  Results take the inputs' place in
+// shared memory and leave by TMA.  The tile after next is on its way (TMA,
+// three stages) while one is computed.
+//
+// A chain is walked by a cluster of 1 to 8 blocks in turn, so that few chains
+// fill the machine too: while one block writes a tile, the next have folded
+// theirs, and what enters them passes from block to block through distributed
+// shared memory, one multiply-add per tile.  Very few chains (kJoin): tiles
+// are drawn by ticket in the order of the rows by all blocks; each publishes
+// its (A, Bs), the last of every kGroup tiles the state that leaves them, and a
+// tile folds the pairs of the earlier ones of its group onto the state that
+// left the group before.  What is waited for belongs to a lower ticket, hence
+// to a block that is running; the words handed on are their own flags (all
+// bits set = not yet written), so one trip to L2 sees and fetches them.  The
+// order of the fold depends on the sizes alone, so the bits are the same every
+// time.
+//
+// The 8-bit checkpoint needs the largest magnitude of a row's 128 channels,
+// several chains: a second kernel writes it, each block for itself, from the
+// states that the first leaves at every unit of rows.
 #include <cudaTypedefs.h>
 #include <cuda_fp8.h>
 
@@ -51,8 +60,9 @@ constexpr int kBlock = 128;     // channels per scale of the checkpoint
 constexpr int kWarps = 8;
 constexpr int kThreads = 32 * kWarps;
 constexpr int kGroup = 16;      // few chains: tiles from one published state to the next
-constexpr int kManyChains = 128;   // from so many chains on, each is walked by one block
-constexpr int kInOrderRows = 512;  // and chains of so few rows are, too
+constexpr int kCluster = 8;     // blocks that walk a chain together, at most
+constexpr int kJoinChains = 16; // fewer chains, of more than
+constexpr int kJoinTiles = 32;  // so many tiles each, are joined tile by tile
 constexpr int kInfoPad = 512;   // rows of padding behind the packed sequences' row information
 constexpr uint32_t kEmpty = 0xffffffffu;     // a word not yet written
 constexpr uint64_t kGiveUp = 2000000000;     // ns after which a wait gives up
@@ -285,8 +295,21 @@ __device__ __forceinline__ void bring(uint8_t* dst, const IO* src, int n, bool w
 
 // ------------------------------------------------------------- pairs (A, Bs)
 __device__ __forceinline__ bool fresh(float A) { return __float_as_uint(A) == 0x80000000u; }
-// What leaves a stretch (A, B) that c enters.
-__device__ __forceinline__ float through(float c, float A, float B) { return fresh(A) ? B : fmaf(A, c, B); }
+// What leaves a stretch (A, B) that c enters; and a stretch followed by another.
+__device__ __forceinline__ float through(float c, float2 s) { return fresh(s.x) ? s.y : fmaf(s.x, c, s.y); }
+__device__ __forceinline__ float2 joined(float2 a, float2 b) {
+  return make_float2(fresh(b.x) ? b.x : a.x * b.x, through(a.y, b));
+}
+
+// A float to the same place in the shared memory of block `rank` of the cluster, counted by the barrier there.
+__device__ __forceinline__ void send(float* place, uint64_t* bar, uint32_t rank, float v) {
+  uint32_t to, at;
+  asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(to) : "r"(smem_u32(place)), "r"(rank));
+  asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(at) : "r"(smem_u32(bar)), "r"(rank));
+  asm volatile("st.async.weak.shared::cluster.mbarrier::complete_tx::bytes.b32 [%0], %1, [%2];" ::"r"(to),
+               "r"(__float_as_uint(v)), "r"(at)
+               : "memory");
+}
 
 // Words handed from block to block through L2: each is its own flag.
 __device__ __forceinline__ void publish(float* p, float v) {
@@ -300,26 +323,22 @@ __device__ __forceinline__ uint32_t peek(const float* p) {
 }
 
 // ------------------------------------------------------------------ the tiles
-enum Kind { kFwd, kFwdCkpt, kBwd, kBwdCkpt };
+enum Kind { kFwd, kBwd, kBwdCkpt };
 
 // Tiles.  A thread holds two channels x one segment of kR rows; kR is odd, so
 // that the segments side by side in a warp lie in different banks, and as
 // large as registers and the stages of two blocks in an SM's shared memory
-// allow.  A unit of a tile is what is folded before the next level: the
-// segments of a warp (16 channels; 32 from the checkpoint, whose codes are one
-// byte), or, in the forward that writes the checkpoint, which needs a row's
-// whole scale block, the one segment of two warps (128 channels); its tile has
-// as many rows as a unit of the forward that does not, so that chains walked
-// in order get the same bits from both.
+// allow.  Rows are 64 bytes of bf16 or fp32; 128 from the checkpoint, whose
+// codes are one byte.
 template <Kind K, typename IO, bool COMPL>
 struct Shape {
-  static constexpr bool kDown = K == kBwd || K == kBwdCkpt, kWide = K == kFwdCkpt;
-  static constexpr int W = kWide ? 128 : K == kBwdCkpt ? 32 : 16;
+  static constexpr bool kDown = K != kFwd;
+  static constexpr int W = sizeof(IO) == 4 ? (K == kBwdCkpt ? 32 : 16) : K == kBwdCkpt ? 64 : 32;
+  static constexpr int kCh = W > 32 ? 2 : 1;                       // channels of a lane on the ways between levels
   static constexpr int kR = sizeof(IO) == 4 || K == kBwd ? 7 : K == kBwdCkpt ? 13 : 15;
   static constexpr int kAcross = W / 2;                            // threads of a row
-  static constexpr int kSide = kWide ? 1 : 32 / kAcross;           // segments of a unit
-  static constexpr int kUnits = kWide ? kThreads / kAcross : kWarps;
-  static constexpr int kUnitRows = kSide * kR, kL = kUnits * kUnitRows;
+  static constexpr int kSide = 32 / kAcross;                       // segments of a unit
+  static constexpr int kUnitRows = kSide * kR, kL = kWarps * kUnitRows;
   static constexpr int kBox = kL <= 256 ? kL : kL / 2;             // rows of one TMA load
   // input arrays: forward x, g; backward dy, g, h, x; from the checkpoint dy, lambda, z
   static constexpr int kIn = K == kBwd ? (COMPL ? 4 : 3) : K == kBwdCkpt ? 3 : 2;
@@ -340,26 +359,28 @@ struct Shape {
 struct TileArgs {
   ScanArgs a;
   CUtensorMap map[4];       // inputs: a tile
-  CUtensorMap out[3];       // h or dL/dx, dL/dg: a unit; with a checkpoint h, lambda and z codes
+  CUtensorMap out[2];       // h or dL/dx, dL/dg: a unit
   WorkspaceHeader* hdr;     // error word; pad[0] is the ticket
-  float* pairs;             // [chains][chunks][2][W]
-  float* states;            // [chains][groups][W]
+  float* pairs;             // kJoin: [chains][chunks][2][W]
+  float* states;            // kJoin: [chains][groups][W]
+  float* enters;            // with a checkpoint: [chains][chunks * kWarps][W], what enters each unit, else null
   const int32_t* info;      // packed: sequence * 4 + first * 2 + last of each row, -1 outside
   int chains, chunks, groups, blocks;  // blocks: of channels
-  bool tma, vec, words, in_order;
+  int cluster;              // blocks that walk a chain; 0: kJoin
+  bool tma, vec, words;
 };
 
 template <typename S>
 struct __align__(128) Shared {
-  float seg[S::kUnits][S::kSide][2][S::W];    // (A, Bs) of the segments, where a unit has several
-  float enter[S::kUnits][S::kSide][S::W];     // what enters them
-  float pair[2][S::kUnits][2][S::W];          // (A, Bs) of the units, of two tiles
-  float into[S::kUnits][S::W];                // few chains: what enters them
-  float carry[2][S::W];                       // in order: what leaves a tile
-  uint32_t top[S::kWide ? kWarps : 1][2][16]; // checkpoint: largest magnitudes of a warp's rows
-  float scale_of[S::kWide ? 1 : kWarps][2][32];  // from the checkpoint: scales of a warp's rows
+  float2 seg[kWarps][S::kSide][S::W];      // (A, Bs) of the segments
+  float enter[kWarps][S::kSide][S::W];     // what enters them
+  float2 pair[2][kWarps][S::W];            // (A, Bs) of the units, of two tiles
+  float into[kWarps][S::W];                // kJoin: what enters them
+  float inbox[2][S::W];                    // else: what enters the tile, of two tiles
+  uint64_t came[2];
+  float scale_of[kWarps][2][32];           // from the checkpoint: scales of a unit's rows
   uint64_t full[S::kStages];
-  int4 tile[S::kStages];                      // chain, chunk (-1: none left), batch, channel block
+  int4 tile[S::kStages];                   // first row, chunk (-1: none left), batch, channel block
   __align__(16) int info[S::kStages][S::kL];
   __align__(16) uint8_t scale[S::kStages][2][(S::kL + 47) / 16 * 16];
 };
@@ -373,24 +394,32 @@ template <Kind K, typename IO, bool RAW, bool COMPL>
 __global__ void __launch_bounds__(kThreads, Shape<K, IO, COMPL>::kPerSm)
     scan_tile_kernel(const __grid_constant__ TileArgs p) {
   using S = Shape<K, IO, COMPL>;
-  constexpr int W = S::W, R = S::kR, L = S::kL, NS = S::kStages, NU = S::kUnits;
-  constexpr bool kDown = S::kDown, kSave = K == kFwdCkpt, kFrom = K == kBwdCkpt;
+  constexpr int W = S::W, R = S::kR, L = S::kL, NS = S::kStages;
+  constexpr bool kDown = S::kDown, kFrom = K == kBwdCkpt;
   extern __shared__ __align__(128) uint8_t stages[];
   __shared__ Shared<S> sh;
   const ScanArgs& a = p.a;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  // this thread's unit and segment of it (in the order of the recurrence), and its two channels
-  const int unit = S::kWide ? (int)threadIdx.x / S::kAcross : warp, side = S::kWide ? 0 : lane / S::kAcross;
-  const int across = (int)threadIdx.x % S::kAcross;
+  // this thread's segment of its warp's rows (in the order of the recurrence), and its two channels
+  const int side = lane / S::kAcross, across = lane % S::kAcross;
   const size_t rows = (size_t)a.B * a.T;
   const bool packed = a.cu != nullptr;
 
   if (threadIdx.x == 0) {
     for (int s = 0; s < NS; ++s) mbar_init(&sh.full[s], 1);
+    for (int s = 0; s < 2; ++s) mbar_init(&sh.came[s], 1);
     fence_mbar_init();
   }
-  __syncthreads();
+  const bool walk = p.cluster > 0;
+  const uint32_t size = walk ? p.cluster : 1, rank = walk ? blockIdx.x % size : 0;
+  __syncwarp();
+  if (size > 1) {
+    asm volatile("barrier.cluster.arrive.release.aligned;\n barrier.cluster.wait.acquire.aligned;" ::: "memory");
+  } else {
+    __syncthreads();
+  }
   grid_dep_wait();  // the workspace was prepared, and the inputs written, by earlier kernels
+  if (walk && p.hdr && blockIdx.x == 0 && threadIdx.x == 0) p.hdr->error = 0;
 
   auto gave_up = [&](uint32_t where) {
     if (!p.hdr) return;
@@ -399,49 +428,67 @@ __global__ void __launch_bounds__(kThreads, Shape<K, IO, COMPL>::kPerSm)
   };
   // where a tile lies
   struct Place {
-    int chain, chunk, b, cb, c, n, s;  // batch, channel block; this lane's first channel, how many from it on; stage
-    int64_t t0;
+    int t0, chunk, b, cb, s;  // first row, number in its chain, batch, channel block, stage
+    int c, n;                 // this thread's first channel, how many the row has from it on
     uint8_t* st;
   };
   auto place_of = [&](int k, int4 tile) {
     Place q;
-    q.chain = tile.x, q.chunk = tile.y, q.b = tile.z, q.cb = tile.w;
-    q.t0 = (kDown ? p.chunks - 1 - q.chunk : q.chunk) * (int64_t)L;
+    q.t0 = tile.x, q.chunk = tile.y, q.b = tile.z, q.cb = tile.w;
     q.c = q.cb * W + across * 2, q.n = a.D - q.c;
     q.s = k % NS, q.st = stages + q.s * S::kStage;
     return q;
   };
+  auto chain_of = [&](const Place& q) { return (size_t)q.b * p.blocks + q.cb; };
   const ScanCkptLayout lay = scan_ckpt_layout(rows, a.D);
   auto scale_at = [&](const Place& q) { return (size_t)(q.cb * W / kBlock) * rows + (size_t)q.b * a.T + q.t0; };
 
-  // ---- warp 0, lane 0: the k-th tile of this block into its stage
-  uint32_t drawn = 0;  // the next ticket
-  int4 next = make_int4((int)blockIdx.x, 0, (int)blockIdx.x / p.blocks, (int)blockIdx.x % p.blocks);
-  if (threadIdx.x == 0 && !p.in_order) drawn = atomicAdd(&p.hdr->pad[0], 1u);
-  auto feed = [&](int k) {
-    if (next.y < 0) return;
-    const int s = k % NS;
-    if (!p.in_order) {
-      const bool there = drawn < (uint32_t)p.chains * (uint32_t)p.chunks;
-      next.y = there ? (int)(drawn / (uint32_t)p.chains) : -1;
-      next.x = (int)(drawn % (uint32_t)p.chains);
-      next.z = next.x / p.blocks, next.w = next.x % p.blocks;
-      if (there) drawn = atomicAdd(&p.hdr->pad[0], 1u);
+  // ---- thread 0: the tiles of this block one after the other
+  uint32_t drawn = 0;  // kJoin: the next ticket
+  const int my_chain = (int)(blockIdx.x / size);
+  int4 next = make_int4(0, (int)rank - (int)size, my_chain / p.blocks, my_chain % p.blocks);
+  if (threadIdx.x == 0 && !walk) next.y = 0, drawn = atomicAdd(&p.hdr->pad[0], 1u);
+  bool more = true;
+  auto advance = [&]() {
+    if (!more) return next;
+    if (walk) {
+      next.y += size;
+      more = next.y < p.chunks;
     } else {
-      next.y = k < p.chunks ? k : -1;
+      more = drawn < (uint32_t)p.chains * (uint32_t)p.chunks;
+      if (more) {
+        const int chain = (int)(drawn % (uint32_t)p.chains);
+        next.y = (int)(drawn / (uint32_t)p.chains);
+        next.z = chain / p.blocks, next.w = chain % p.blocks;
+        drawn = atomicAdd(&p.hdr->pad[0], 1u);
+      }
     }
-    sh.tile[s] = next;
-    if (next.y < 0) {
+    if (!more) next.y = -1;
+    next.x = (kDown ? p.chunks - 1 - next.y : next.y) * L;
+    return next;
+  };
+  // walk: the barrier of the k-th tile's state; the chain's first tile has none.  A block that walks alone
+  // writes its own state and arrives by itself.
+  auto expect = [&](int k, bool first) {
+    if (first)
+      mbar_arrive(&sh.came[k & 1]);
+    else if (size > 1)
+      mbar_expect_tx(&sh.came[k & 1], W * 4);
+  };
+  // ---- thread 0: the k-th tile into its stage
+  auto feed = [&](int k, int4 tile) {
+    const int s = k % NS;
+    sh.tile[s] = tile;
+    if (tile.y < 0) {
       mbar_arrive(&sh.full[s]);
       return;
     }
-    const Place q = place_of(k, next);
+    const Place q = place_of(k, tile);
     constexpr uint32_t kArray = L * W * sizeof(IO);  // an array in the caller's type
     uint32_t bytes = (p.tma ? (kFrom ? 1 : S::kIn) * kArray : 0) + (kFrom ? 2 * L * W : 0) + (packed ? L * 4 : 0);
     uint32_t scale_bytes = 0;
     if (kFrom) {
-      const uint32_t valid = (uint32_t)min((int64_t)L, a.T - q.t0);
-      scale_bytes = ((uint32_t)(scale_at(q) & 15) + valid + 15) & ~15u;
+      scale_bytes = ((uint32_t)(scale_at(q) & 15) + (uint32_t)min(L, a.T - q.t0) + 15) & ~15u;
       bytes += 2 * scale_bytes;
     }
     if (bytes)
@@ -454,7 +501,7 @@ __global__ void __launch_bounds__(kThreads, Shape<K, IO, COMPL>::kPerSm)
 #pragma unroll
         for (int part = 0; part < L / S::kBox; ++part)  // h one row up: what enters each row
           tma_load_3d(q.st + S::at(i) + part * S::kBox * W * S::eb(i), &p.map[i], &sh.full[s], q.cb * W,
-                      (int)q.t0 + part * S::kBox - (K == kBwd && i == 2 ? 1 : 0), q.b);
+                      q.t0 + part * S::kBox - (K == kBwd && i == 2 ? 1 : 0), q.b);
     if (packed) bulk_load(sh.info[s], p.info + q.t0, L * 4, &sh.full[s]);
     if (kFrom) {
       const size_t at = scale_at(q) & ~size_t(15);
@@ -462,7 +509,11 @@ __global__ void __launch_bounds__(kThreads, Shape<K, IO, COMPL>::kPerSm)
       bulk_load(sh.scale[s][1], a.ckpt + lay.z_scale + at, scale_bytes, &sh.full[s]);
     }
   };
-  if (threadIdx.x == 0) feed(0), feed(1);
+  if (threadIdx.x == 0) {
+    feed(0, advance()), feed(1, advance());
+    advance();
+    if (walk) expect(0, rank == 0), expect(1, false);
+  }
 
   // the k-th tile of this block, chunk -1 past its last
   auto tile_of = [&](int k) {
@@ -472,10 +523,10 @@ __global__ void __launch_bounds__(kThreads, Shape<K, IO, COMPL>::kPerSm)
   };
   // the r-th row of this thread's segment, as a row of the tile
   auto row_at = [&](int r) {
-    const int i = unit * S::kUnitRows + side * R + r;
+    const int i = warp * S::kUnitRows + side * R + r;
     return kDown ? L - 1 - i : i;
   };
-  const int lowest = kDown ? L - (unit + 1) * S::kUnitRows : unit * S::kUnitRows;  // row of the unit
+  const int lowest = kDown ? L - (warp + 1) * S::kUnitRows : warp * S::kUnitRows;  // row of the unit
   auto elem = [&](const Place& q, int arr, int i) { return q.st + S::at(arr) + (i * W + across * 2) * S::eb(arr); };
   auto global_row = [&](const Place& q, int i) { return (size_t)q.b * a.T + q.t0 + i; };
   auto row_info = [&](const Place& q, int i) {
@@ -484,7 +535,7 @@ __global__ void __launch_bounds__(kThreads, Shape<K, IO, COMPL>::kPerSm)
       const int v = sh.info[q.s][i];
       o.valid = v >= 0, o.first = v & 2, o.last = v & 1, o.seq = v >> 2;
     } else {
-      const int64_t t = q.t0 + i;
+      const int t = q.t0 + i;
       o.valid = t < a.T, o.first = t == 0, o.last = t == a.T - 1, o.seq = q.b;
     }
     return o;
@@ -546,7 +597,21 @@ __global__ void __launch_bounds__(kThreads, Shape<K, IO, COMPL>::kPerSm)
     const Place q = place_of(k, tile);
     // rows out of the ordinary: none in most tiles
     const bool edge = has_edge(q) || !p.tma;
-    float(*pair)[2][W] = sh.pair[k & 1];
+    float2(*pair)[W] = sh.pair[k & 1];
+    constexpr int kCh = S::kCh;
+    const int ch = kCh * lane % W;  // on the ways between segment, unit and tile; with 16 channels half of a warp repeats the other
+    auto arrived = [&](const float* at, uint32_t v) {
+      if (v == kEmpty && !failed) {
+        const uint64_t since = now_ns();
+        while ((v = peek(at)) == kEmpty)
+          if (now_ns() - since > kGiveUp) {
+            failed = true;
+            gave_up(203);
+            break;
+          }
+      }
+      return __uint_as_float(v);
+    };
     if constexpr (kFrom) {
       if (lane < S::kUnitRows) {
         const int off = (int)(scale_at(q) & 15) + lowest + lane;
@@ -582,64 +647,77 @@ __global__ void __launch_bounds__(kThreads, Shape<K, IO, COMPL>::kPerSm)
           B = kDown ? mul2(al[r], add2(B, x)) : fma2(al[r], B, in[r]);
         }
       }
-      float(*to)[W] = S::kSide == 1 ? pair[unit] : sh.seg[unit][side];
-      float f[2];
-      unpack(A, f[0], f[1]);
-      sts<2>(&to[0][across * 2], f);
-      unpack(B, f[0], f[1]);
-      sts<2>(&to[1][across * 2], f);
+      float4 f;
+      unpack(A, f.x, f.z);
+      unpack(B, f.y, f.w);
+      *reinterpret_cast<float4*>(S::kSide == 1 ? &pair[warp][across * 2] : &sh.seg[warp][side][across * 2]) = f;
     };
     if (edge)
       reduce(std::true_type{});
     else
       reduce(std::false_type{});
+    [[maybe_unused]] float2 sg[S::kSide];
     if constexpr (S::kSide > 1) {  // the unit's pair
       __syncwarp();
-      if (lane < W) {
-        float ta = sh.seg[warp][0][0][lane], tb = sh.seg[warp][0][1][lane];
 #pragma unroll
-        for (int g = 1; g < S::kSide; ++g) {
-          const float wa = sh.seg[warp][g][0][lane], wb = sh.seg[warp][g][1][lane];
-          tb = through(tb, wa, wb);
-          ta = fresh(wa) ? wa : ta * wa;
-        }
-        pair[warp][0][lane] = ta, pair[warp][1][lane] = tb;
-      }
+      for (int g = 0; g < S::kSide; ++g) sg[g] = sh.seg[warp][g][ch];
+      float2 t = sg[0];
+#pragma unroll
+      for (int g = 1; g < S::kSide; ++g) t = joined(t, sg[g]);
+      pair[warp][ch] = t;
     }
     if (lane == 0) bulk_wait_read();  // the tile before has left its stage
     __syncthreads();  // the pairs are there, and every warp is done with the tile before
-    if (threadIdx.x == 0) feed(k + 2);  // into its stage
+    if (threadIdx.x == 0) {
+      if (walk && k > 0) expect(k + 1, false);
+      feed(k + 2, next);  // into its stage
+    }
 
-    // ---- few chains: what enters the units, one thread per channel
-    if (!p.in_order) {
-      const int place = q.chunk % kGroup;
-      if (warp < (W + 31) / 32) {  // with 16 channels both halves of the warp do the same
-        const int ch = threadIdx.x % W;
-        float* state = p.states + ((size_t)q.chain * p.groups + q.chunk / kGroup) * W + ch;
-        float* pairs = p.pairs + ((size_t)q.chain * p.chunks + q.chunk) * (2 * W) + ch;
-        auto arrived = [&](const float* at, uint32_t v) {
-          if (v == kEmpty && !failed) {
-            const uint64_t since = now_ns();
-            while ((v = peek(at)) == kEmpty)
-              if (now_ns() - since > kGiveUp) {
-                failed = true;
-                gave_up(203);
-                break;
-              }
-          }
-          return __uint_as_float(v);
-        };
-        uint32_t head = 0;
-        if (q.chunk >= kGroup) head = peek(state - W);
-        float ta = pair[0][0][ch], tb = pair[0][1][ch];
+    // ---- what enters the tile
+    float e[kCh];
+    if (walk) {
+      float2 t[kCh];  // warp 0: the tile's pair
+      if (warp == 0) {
 #pragma unroll
-        for (int w = 1; w < NU; ++w) {
-          const float wa = pair[w][0][ch], wb = pair[w][1][ch];
-          tb = through(tb, wa, wb);
-          ta = fresh(wa) ? wa : ta * wa;
+        for (int j = 0; j < kCh; ++j) {
+          t[j] = pair[0][ch + j];
+#pragma unroll
+          for (int w = 1; w < kWarps; ++w) t[j] = joined(t[j], pair[w][ch + j]);
         }
-        if (place != kGroup - 1 && q.chunk != p.chunks - 1) publish(pairs, ta), publish(pairs + W, tb);
-        float ga = 1.f, gb = 0.f;  // the group's earlier tiles
+      }
+      if (!wait_for(&sh.came[k & 1], (k >> 1) & 1)) gave_up(204);
+#pragma unroll
+      for (int j = 0; j < kCh; ++j) e[j] = q.chunk > 0 ? sh.inbox[k & 1][ch + j] : 0.f;
+      if (warp == 0 && q.chunk + 1 < p.chunks) {  // on to the block that has the next tile
+        const bool wraps = rank + 1 == size;
+        const int there = wraps ? k + 1 : k;
+#pragma unroll
+        for (int j = 0; j < kCh; ++j) {
+          const float out = through(e[j], t[j]);
+          if (size == 1)
+            sh.inbox[there & 1][ch + j] = out;
+          else if (lane < W)
+            send(&sh.inbox[there & 1][ch + j], &sh.came[there & 1], wraps ? 0 : rank + 1, out);
+        }
+        __syncwarp();
+        if (size == 1 && lane == 0) mbar_arrive(&sh.came[there & 1]);
+      }
+      for (int w = 0; w < warp; ++w)
+#pragma unroll
+        for (int j = 0; j < kCh; ++j) e[j] = through(e[j], pair[w][ch + j]);
+    } else {
+      const int place = q.chunk % kGroup;
+      if (threadIdx.x < (W > 32 ? W : 32)) {  // one thread per channel
+        const int c1 = threadIdx.x % W;
+        float* state = p.states + (chain_of(q) * p.groups + q.chunk / kGroup) * W + c1;
+        float* pairs = p.pairs + (chain_of(q) * p.chunks + q.chunk) * (2 * W) + c1;
+        uint32_t before = 0;
+        if (q.chunk >= kGroup) before = peek(state - W);
+        float2 t = pair[0][c1];
+#pragma unroll
+        for (int w = 1; w < kWarps; ++w) t = joined(t, pair[w][c1]);
+        if (place != kGroup - 1 && q.chunk != p.chunks - 1) publish(pairs, t.x), publish(pairs + W, t.y);
+        float2 g = make_float2(1.f, 0.f);  // the group's earlier tiles
         constexpr int kBatch = 5;
         for (int k0 = 0; k0 < place; k0 += kBatch) {
           const float* at = pairs - (size_t)(place - k0) * (2 * W);
@@ -651,67 +729,41 @@ __global__ void __launch_bounds__(kThreads, Shape<K, IO, COMPL>::kPerSm)
           for (int i = 0; i < kBatch; ++i)
             if (k0 + i < place) {
               const float ka = arrived(at + i * 2 * W, va[i]), kb = arrived(at + i * 2 * W + W, vb[i]);
-              gb = through(gb, ka, kb);
-              ga = fresh(ka) ? ka : ga * ka;
+              g = joined(g, make_float2(ka, kb));
             }
         }
-        float h = q.chunk >= kGroup ? arrived(state - W, head) : 0.f;
-        h = through(h, ga, gb);
-        if (place == kGroup - 1) publish(state, through(h, ta, tb));
+        float h = q.chunk >= kGroup ? arrived(state - W, before) : 0.f;
+        h = through(h, g);
+        if (place == kGroup - 1) publish(state, through(h, t));
 #pragma unroll
-        for (int w = 0; w < NU; ++w) {
-          sh.into[w][ch] = h;
-          h = through(h, pair[w][0][ch], pair[w][1][ch]);
+        for (int w = 0; w < kWarps; ++w) {
+          sh.into[w][c1] = h;
+          h = through(h, pair[w][c1]);
         }
       }
       __syncthreads();
+#pragma unroll
+      for (int j = 0; j < kCh; ++j) e[j] = sh.into[warp][ch + j];
     }
 
-    // ---- what enters this thread's segment
+    // ---- what enters the unit, then this thread's segment
+    if (K == kFwd && p.enters) {
+#pragma unroll
+      for (int j = 0; j < kCh; ++j)
+        p.enters[((chain_of(q) * p.chunks + q.chunk) * kWarps + warp) * W + ch + j] = e[j];
+    }
     f2 h;  // forward: the state, backward: c_{t+1}
-    {
-      constexpr int kMine = S::kWide ? 2 : 1;  // channels of a thread on this way
-      if (S::kWide || lane < W) {
-        const int ch = S::kWide ? across * 2 : lane;
-        float e[2];
+    if constexpr (S::kSide == 1) {
+      h = pack(e[0], e[kCh - 1]);
+    } else {
 #pragma unroll
-        for (int j = 0; j < kMine; ++j) {
-          if (!p.in_order) {
-            e[j] = sh.into[unit][ch + j];
-          } else {
-            e[j] = k > 0 ? sh.carry[k & 1][ch + j] : 0.f;
-            if constexpr (S::kWide) {  // the tile is one unit of the other forward: its carry goes through the whole
-              if (unit == NU - 1) {
-                float fa = pair[0][0][ch + j], fb = pair[0][1][ch + j];
-#pragma unroll
-                for (int w = 1; w < NU; ++w) {
-                  const float wa = pair[w][0][ch + j], wb = pair[w][1][ch + j];
-                  fb = through(fb, wa, wb);
-                  fa = fresh(wa) ? wa : fa * wa;
-                }
-                sh.carry[(k + 1) & 1][ch + j] = through(e[j], fa, fb);
-              }
-            }
-            for (int w = 0; w < unit; ++w) e[j] = through(e[j], pair[w][0][ch + j], pair[w][1][ch + j]);
-            if (!S::kWide && unit == NU - 1)
-              sh.carry[(k + 1) & 1][ch + j] = through(e[j], pair[unit][0][ch + j], pair[unit][1][ch + j]);
-          }
-        }
-        if constexpr (S::kWide) {
-          h = pack(e[0], e[1]);
-        } else {
-#pragma unroll
-          for (int g = 0; g < S::kSide; ++g) {
-            sh.enter[warp][g][lane] = e[0];
-            e[0] = through(e[0], sh.seg[warp][g][0][lane], sh.seg[warp][g][1][lane]);
-          }
-        }
+      for (int g = 0; g < S::kSide; ++g) {
+        sh.enter[warp][g][ch] = e[0];
+        e[0] = through(e[0], sg[g]);
       }
-      if constexpr (!S::kWide) {
-        __syncwarp();
-        const float2 e = *reinterpret_cast<const float2*>(&sh.enter[warp][side][across * 2]);
-        h = pack(e.x, e.y);
-      }
+      __syncwarp();
+      const float2 v = *reinterpret_cast<const float2*>(&sh.enter[warp][side][across * 2]);
+      h = pack(v.x, v.y);
     }
 
     // ---- the rows themselves, results into the stage
@@ -735,7 +787,6 @@ __global__ void __launch_bounds__(kThreads, Shape<K, IO, COMPL>::kPerSm)
         const int i = row_at(r);
         const Row o = E ? row_info(q, i) : Row{true, false, false, 0};
         if (E && !o.valid) {  // past the end, or a row that no sequence owns
-          al[r] = in[r] = both(0.f);
           if (!direct || q.t0 + i < a.T) {
             store(static_cast<IO*>(a.out), elem(q, 0, i), i, both(0.f), direct);
             if (kDown) store(static_cast<IO*>(a.dg), second(i), i, both(0.f), direct);
@@ -744,20 +795,8 @@ __global__ void __launch_bounds__(kThreads, Shape<K, IO, COMPL>::kPerSm)
         }
         const bool start = E && (kDown ? o.last : o.first);
         if constexpr (!kDown) {
-          [[maybe_unused]] f2 z, lam;
-          if constexpr (kSave) {
-            z = start ? state_of(q, a.s0, o.seq) : h;
-            if (COMPL) z = add2(z, neg2(load2(q, 0, i)));
-            lam = load2(q, 1, i);
-            if (RAW) {
-              float l0, l1;
-              unpack(lam, l0, l1);
-              lam = pack(q.n > 0 ? log_sigmoid(l0) : 0.f, q.n > 1 ? log_sigmoid(l1) : 0.f);
-            }
-          }
           h = start ? in[r] : fma2(al[r], h, in[r]);
           store(static_cast<IO*>(a.out), elem(q, 0, i), i, h, direct);
-          if constexpr (kSave) al[r] = lam, in[r] = z;
         } else {
           f2 z;
           if constexpr (kFrom) z = codes_of(q, 2, i);
@@ -786,51 +825,165 @@ __global__ void __launch_bounds__(kThreads, Shape<K, IO, COMPL>::kPerSm)
     else
       emit(std::false_type{});
 
-    if constexpr (kSave) {
-      // ---- al and in hold lambda and z now: the rows' scales, then the codes into g's place, unit by unit
-      float v[2];
-#pragma unroll
-      for (int r = 0; r < R; ++r) {
-#pragma unroll
-        for (int m = 0; m < 2; ++m) {
-          unpack(m ? in[r] : al[r], v[0], v[1]);
-          const uint32_t top = __reduce_max_sync(0xffffffffu, max(magnitude(v[0]), magnitude(v[1])));
-          if (lane == 0) sh.top[warp][m][r] = top;
-        }
-      }
-      named_bar_sync(1 + unit, S::kAcross);
-      uint8_t* codes = q.st + S::at(1) + unit * S::kUnitRows * W * (int)sizeof(IO);
-#pragma unroll
-      for (int r = 0; r < R; ++r) {
-#pragma unroll
-        for (int m = 0; m < 2; ++m) {
-          const int code = scale_code(__uint_as_float(max(sh.top[warp][m][r], sh.top[warp ^ 1][m][r])));
-          unpack(m ? in[r] : al[r], v[0], v[1]);
-          *reinterpret_cast<uint16_t*>(codes + (m * R + r) * W + across * 2) = encode2(v, pow2(254 - code));
-          if (across == r && q.t0 + row_at(r) < a.T)
-            a.ckpt[(m ? lay.z_scale : lay.lam_scale) + q.cb * rows + global_row(q, row_at(r))] = (uint8_t)code;
-        }
-      }
-    }
     // ---- out by TMA, each unit's rows (rows past T are not written)
-    fence_async_smem();
-    if constexpr (S::kWide)
-      named_bar_sync(1 + unit, S::kAcross);
-    else
+    if (p.tma) {
+      fence_async_smem();
       __syncwarp();
-    if ((S::kWide ? across == 0 : lane == 0) && q.t0 + lowest < a.T) {
-      const int c0 = q.cb * W, t = (int)q.t0 + lowest;
-      const auto leave = [&](const CUtensorMap& map, const uint8_t* from) { tma_store_3d(&map, from, c0, t, q.b); };
-      const int at = lowest * W * (int)sizeof(IO);
-      if (p.tma) {
-        leave(p.out[0], q.st + at);
-        if (kDown) leave(p.out[1], (kFrom ? stages + NS * S::kStage : q.st + S::at(1)) + at);
+      if (lane == 0 && q.t0 + lowest < a.T) {
+        const int at = lowest * W * (int)sizeof(IO), t = q.t0 + lowest;
+        tma_store_3d(&p.out[0], q.st + at, q.cb * W, t, q.b);
+        if (kDown) tma_store_3d(&p.out[1], (kFrom ? stages + NS * S::kStage : q.st + S::at(1)) + at, q.cb * W, t, q.b);
+        bulk_commit();
       }
-      if (kSave) leave(p.out[1], q.st + S::at(1) + at), leave(p.out[2], q.st + S::at(1) + at + R * W);
-      bulk_commit();
     }
+    if (threadIdx.x == 0) advance();
   }
   if (lane == 0) bulk_wait_read();
+  __syncwarp();
+  // a block's shared memory stays until the others have sent what they send
+  if (size > 1) asm volatile("barrier.cluster.arrive.release.aligned;\n barrier.cluster.wait.acquire.aligned;" ::: "memory");
+}
+
+// The 8-bit checkpoint.  A block writes 128 channels (a row's scale block) of
+// four segments of the forward's rows; a thread holds two channels x one
+// segment, as there, and goes the same way from the state that entered the
+// segment's unit, so that z is what the forward saw.  8 B of traffic per
+// element in bf16 (x and g are read once more, from L2 for the rows that the
+// forward did last, which come first here); all loads of a thread are in
+// flight at once.
+template <typename IO, bool RAW, bool COMPL>
+__global__ void __launch_bounds__(256, 2) scan_save_kernel(const __grid_constant__ TileArgs p) {
+  using S = Shape<kFwd, IO, COMPL>;
+  constexpr int R = S::kR, kSegs = 4;
+  __shared__ float2 pair[kSegs][kBlock];
+  __shared__ uint32_t top[8][2][R];
+  __shared__ float inv[kSegs][2][R];
+  const ScanArgs& a = p.a;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, across = threadIdx.x % 64, seg = threadIdx.x / 64;
+  const int kb = (a.D + kBlock - 1) / kBlock, parts = (a.T + kSegs * R - 1) / (kSegs * R);
+  const int cb = blockIdx.x % kb, b = blockIdx.x / kb % a.B, part = parts - 1 - (int)(blockIdx.x / kb / a.B);
+  const int c = cb * kBlock + across * 2, n = a.D - c;
+  const int t0 = (part * kSegs + seg) * R, most = min(R, a.T - t0);  // rows of this thread: the first `most` exist
+  const size_t rows = (size_t)a.B * a.T, row0 = (size_t)b * a.T + t0;
+  const ScanCkptLayout lay = scan_ckpt_layout(rows, a.D);
+  // the rows as loaded, two channels in a word (bf16) or two
+  constexpr int kWords = sizeof(IO) / 2;
+  uint32_t x[R][kWords], g[R][kWords];
+  const bool pairs = a.D % 2 == 0;
+  const IO *px = static_cast<const IO*>(a.x) + row0 * a.D + c, *pg = static_cast<const IO*>(a.g) + row0 * a.D + c;
+  auto load = [&](const IO* q, bool in, uint32_t* to) {
+    if (pairs && in && n > 0) {
+#pragma unroll
+      for (int j = 0; j < kWords; ++j) to[j] = __ldg(reinterpret_cast<const uint32_t*>(q) + j);
+    } else {
+      IO v[2] = {in && n > 0 ? q[0] : from_f32<IO>(0.f), in && n > 1 ? q[1] : from_f32<IO>(0.f)};
+#pragma unroll
+      for (int j = 0; j < kWords; ++j) to[j] = reinterpret_cast<const uint32_t*>(v)[j];
+    }
+  };
+#pragma unroll
+  for (int r = 0; r < R; ++r) {
+    load(px + (size_t)r * a.D, r < most, x[r]);
+    load(pg + (size_t)r * a.D, r < most, g[r]);
+  }
+  auto value = [](const uint32_t* w) {
+    if constexpr (kWords == 1)
+      return pack(__uint_as_float(w[0] << 16), __uint_as_float(w[0] & 0xffff0000u));
+    else
+      return pack(__uint_as_float(w[0]), __uint_as_float(w[1]));
+  };
+  grid_dep_wait();  // what entered the units comes from the kernel before
+  // bit r: whether row r belongs to a sequence, and whether it is one's first
+  uint32_t valid = most > 0 ? (1u << most) - 1 : 0, first = t0 == 0 ? 1 : 0;
+  if (a.cu) {
+    valid = first = 0;
+    for (int r = 0; r < most; ++r) {
+      const int v = __ldg(p.info + t0 + r);
+      valid |= (v >= 0 ? 1u : 0u) << r, first |= (v >= 0 && (v & 2) ? 1u : 0u) << r;
+    }
+  }
+  auto state_of = [&](int r) {
+    float v[2];
+    const int seq = a.cu ? __ldg(p.info + t0 + r) >> 2 : b;
+    ldg<2>(a.s0 ? a.s0 + (size_t)seq * a.D + c : nullptr, v, n, pairs);
+    return pack(v[0], v[1]);
+  };
+  float f[2] = {0.f, 0.f};
+  const int unit = part * (kSegs / S::kSide) + seg / S::kSide;
+  if (n > 0 && unit < p.chunks * kWarps) {
+    const size_t chain = (size_t)b * p.blocks + c / S::W;
+    const float2 e = *reinterpret_cast<const float2*>(p.enters + (chain * p.chunks * kWarps + unit) * S::W + c % S::W);
+    f[0] = e.x, f[1] = e.y;
+  }
+  {
+    f2 A = both(1.f), B = both(0.f);
+#pragma unroll
+    for (int r = 0; r < R; ++r) {
+      f2 al, be;
+      gate<RAW>(value(g[r]), al, be);
+      const f2 in = COMPL ? mul2(be, value(x[r])) : value(x[r]);
+      if (first >> r & 1) {
+        A = both(-0.f);
+        B = fma2(al, state_of(r), in);
+      } else if (valid >> r & 1) {
+        A = mul2(A, al);
+        B = fma2(al, B, in);
+      }
+    }
+    float4 v;
+    unpack(A, v.x, v.z);
+    unpack(B, v.y, v.w);
+    *reinterpret_cast<float4*>(&pair[seg][across * 2]) = v;
+  }
+  __syncthreads();
+  for (int s = seg / S::kSide * S::kSide; s < seg; ++s)
+#pragma unroll
+    for (int j = 0; j < 2; ++j) f[j] = through(f[j], pair[s][across * 2 + j]);
+  f2 h = pack(f[0], f[1]), z[R];
+#pragma unroll
+  for (int r = 0; r < R; ++r) {
+    f2 al, be;
+    gate<RAW>(value(g[r]), al, be);
+    if (first >> r & 1) h = state_of(r);
+    z[r] = both(0.f);
+    if (valid >> r & 1) {
+      z[r] = COMPL ? add2(h, neg2(value(x[r]))) : h;
+      h = fma2(al, h, COMPL ? mul2(be, value(x[r])) : value(x[r]));
+    }
+    unpack(z[r], f[0], f[1]);
+    const uint32_t m = __reduce_max_sync(0xffffffffu, max(magnitude(f[0]), magnitude(f[1])));
+    if (lane == 0) top[warp][1][r] = m;
+  }
+  f2 lam[R];
+#pragma unroll
+  for (int r = 0; r < R; ++r) {
+    lam[r] = value(g[r]);
+    unpack(lam[r], f[0], f[1]);
+    const bool in = valid >> r & 1;
+    if (RAW) f[0] = log_sigmoid(f[0]), f[1] = log_sigmoid(f[1]);
+    f[0] = in && n > 0 ? f[0] : 0.f, f[1] = in && n > 1 ? f[1] : 0.f;
+    lam[r] = pack(f[0], f[1]);
+    const uint32_t m = __reduce_max_sync(0xffffffffu, max(magnitude(f[0]), magnitude(f[1])));
+    if (lane == 0) top[warp][0][r] = m;
+  }
+  __syncthreads();
+  if (across < 2 * R) {  // one scale each
+    const int m = across / R, r = across % R;
+    const int code = scale_code(__uint_as_float(max(top[2 * seg][m][r], top[2 * seg + 1][m][r])));
+    inv[seg][m][r] = pow2(254 - code);
+    if (r < most) a.ckpt[(m ? lay.z_scale : lay.lam_scale) + cb * rows + row0 + r] = (uint8_t)code;
+  }
+  __syncthreads();
+  if (n <= 0) return;
+  uint8_t* to = a.ckpt + row0 * lay.pitch + c;
+#pragma unroll
+  for (int r = 0; r < R; ++r, to += lay.pitch) {
+    if (r >= most) break;
+    unpack(lam[r], f[0], f[1]);
+    *reinterpret_cast<uint16_t*>(to) = encode2(f, inv[seg][0][r]);
+    unpack(z[r], f[0], f[1]);
+    *reinterpret_cast<uint16_t*>(to + lay.z) = encode2(f, inv[seg][1][r]);
+  }
 }
 
 // Before a sequence call: header and ticket cleared, the words that blocks
@@ -940,28 +1093,55 @@ bool make_map(CUtensorMap* map, const void* base, int eb, int B, int T, size_t w
              CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
-// Whether each chain is walked by one block (no words handed between blocks).
-bool walked(int T, int64_t chains) { return T <= kInOrderRows || chains >= kManyChains; }
-
 int64_t div_up(int64_t a, int64_t b) { return (a + b - 1) / b; }
 size_t align256(size_t v) { return (v + 255) / 256 * 256; }
+size_t info_bytes(int T) { return align256(((size_t)T + kInfoPad) * 4); }
 
-int sm_count() {
-  int dev = 0, n = 0;
-  if (cudaGetDevice(&dev) != cudaSuccess || cudaDeviceGetAttribute(&n, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess)
-    return 148;
-  return n;
+constexpr int kSms = 148;  // of a B200; a launch is sized for it, results do not depend on it
+
+// How a call of these sizes goes: the blocks that walk a chain together (0:
+// kJoin), and what it keeps in the workspace.
+struct Plan {
+  int64_t chains, chunks, groups;
+  int cluster;
+  size_t pair_words, state_words;  // to be marked as not written
+};
+Plan plan_of(int64_t B, int64_t T, int64_t D, int width, int rows, int per_sm) {
+  Plan q{};
+  q.chains = B * div_up(D, width), q.chunks = div_up(T, rows);
+  if (q.chains < kJoinChains && q.chunks > kJoinTiles) {
+    q.groups = div_up(q.chunks, kGroup);
+    q.pair_words = (size_t)(q.chains * q.chunks * 2 * width);
+    q.state_words = (size_t)(q.chains * q.groups * width);
+  } else {
+    q.cluster = 1;
+    while (q.cluster < kCluster && q.chains * q.cluster * 2 <= kSms * per_sm && q.cluster * 2 <= q.chunks) q.cluster *= 2;
+  }
+  return q;
+}
+template <Kind K, typename IO, bool COMPL>
+Plan plan_for(int64_t B, int64_t T, int64_t D) {
+  using S = Shape<K, IO, COMPL>;
+  return plan_of(B, T, D, S::W, S::kL, S::kPerSm);
 }
 
+// `after`: the kernel waits for the one before it by itself; cluster: of so many blocks.
 template <typename... P, typename... A>
 cudaError_t launch(void (*kernel)(P...), unsigned grid, unsigned threads, size_t smem, cudaStream_t stream, bool after,
-                   const A&... args) {
+                   int cluster, const A&... args) {
   cudaLaunchConfig_t cfg{};
   cfg.gridDim = dim3(grid), cfg.blockDim = dim3(threads), cfg.dynamicSmemBytes = smem, cfg.stream = stream;
-  cudaLaunchAttribute attr[1];
-  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  attr[0].val.programmaticStreamSerializationAllowed = 1;
-  cfg.attrs = attr, cfg.numAttrs = after ? 1 : 0;
+  cudaLaunchAttribute attr[2];
+  if (after) {
+    attr[cfg.numAttrs].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[cfg.numAttrs++].val.programmaticStreamSerializationAllowed = 1;
+  }
+  if (cluster > 1) {
+    attr[cfg.numAttrs].id = cudaLaunchAttributeClusterDimension;
+    attr[cfg.numAttrs].val.clusterDim.x = cluster, attr[cfg.numAttrs].val.clusterDim.y = 1;
+    attr[cfg.numAttrs++].val.clusterDim.z = 1;
+  }
+  cfg.attrs = attr;
   return cudaLaunchKernelEx(&cfg, kernel, args...);
 }
 
@@ -970,25 +1150,23 @@ cudaError_t launch_tiles(const ScanArgs& a, void* ws, cudaStream_t stream) {
   using S = Shape<K, IO, COMPL>;
   TileArgs p;
   p.a = a;
+  const Plan plan = plan_for<K, IO, COMPL>(a.B, a.T, a.D);
   p.blocks = (int)div_up(a.D, S::W);
-  const int64_t chains = (int64_t)a.B * p.blocks, chunks = div_up(a.T, S::kL);
-  p.chains = (int)chains, p.chunks = (int)chunks;
-  p.groups = (int)div_up(chunks, kGroup);
-  p.in_order = walked(a.T, chains);
+  p.chains = (int)plan.chains, p.chunks = (int)plan.chunks, p.groups = (int)plan.groups;
+  p.cluster = plan.cluster;
   p.vec = a.D % 4 == 0;
   p.tma = (size_t)a.D * sizeof(IO) % 16 == 0;
   p.words = (size_t)a.D * sizeof(IO) % 4 == 0;
-  // workspace: header, pairs, states, row information (the last two kinds of words only where needed)
   uint8_t* w = static_cast<uint8_t*>(ws);
   p.hdr = reinterpret_cast<WorkspaceHeader*>(w);
   w += sizeof(WorkspaceHeader);
   p.pairs = reinterpret_cast<float*>(w);
-  const size_t pair_words = p.in_order ? 0 : (size_t)(chains * chunks) * (2 * S::W);
-  const size_t state_words = p.in_order ? 0 : (size_t)chains * p.groups * S::W;
-  p.states = p.pairs + pair_words;
-  int32_t* info = reinterpret_cast<int32_t*>(p.states + state_words);
+  p.states = p.pairs + plan.pair_words;
+  w += align256((plan.pair_words + plan.state_words) * 4);
+  int32_t* info = reinterpret_cast<int32_t*>(w);
   p.info = info;
-  if (!ws || (p.in_order && !a.cu)) p.hdr = nullptr;  // no workspace
+  if (a.cu) w += info_bytes(a.T);
+  p.enters = K == kFwd && a.ckpt ? reinterpret_cast<float*>(w) : nullptr;
   const void* arrays[4] = {a.x, a.g, nullptr, nullptr};
   if (S::kDown) arrays[0] = a.dy, arrays[1] = a.g, arrays[2] = a.h, arrays[3] = a.x;
   const ScanCkptLayout l = scan_ckpt_layout((size_t)a.B * a.T, a.D);
@@ -1001,9 +1179,6 @@ cudaError_t launch_tiles(const ScanArgs& a, void* ws, cudaStream_t stream) {
   }
   if (p.tma) ok = ok && make_map(&p.out[0], a.out, sizeof(IO), a.B, a.T, a.D, a.D, S::W, S::kUnitRows);
   if (p.tma && S::kDown) ok = ok && make_map(&p.out[1], a.dg, sizeof(IO), a.B, a.T, a.D, a.D, S::W, S::kUnitRows);
-  if (K == kFwdCkpt)
-    for (int i = 1; i <= 2; ++i)
-      ok = ok && make_map(&p.out[i], a.ckpt + (i == 2 ? l.z : 0), 1, a.B, a.T, a.D, l.pitch, S::W, S::kUnitRows);
   if (!ok) return cudaErrorInvalidValue;
   auto kernel = scan_tile_kernel<K, IO, RAW, COMPL>;
   static std::atomic<uint64_t> ready{0};  // devices whose shared-memory limit has been raised
@@ -1016,39 +1191,51 @@ cudaError_t launch_tiles(const ScanArgs& a, void* ws, cudaStream_t stream) {
     if (e != cudaSuccess) return e;
     ready.fetch_or(bit, std::memory_order_relaxed);
   }
-  const int sms = sm_count();
-  const bool init = !p.in_order || a.cu;
+  const bool init = !p.cluster || a.cu;
   if (init) {
-    const size_t count = (pair_words + state_words) / 4;
-    const int64_t blocks = std::min<int64_t>(std::max<int64_t>(div_up((int64_t)count, 256 * 4), div_up(a.cu ? a.T : 1, 256)), sms * 8);
-    e = launch(scan_init_kernel, (unsigned)std::max<int64_t>(blocks, 1), 256, 0, stream, false, p,
+    const size_t count = (plan.pair_words + plan.state_words) / 4;
+    const int64_t blocks = std::max(div_up((int64_t)count, 256 * 4), div_up(a.cu ? a.T + kInfoPad : 1, 256));
+    e = launch(scan_init_kernel, (unsigned)std::min<int64_t>(blocks, kSms * 8), 256, 0, stream, false, 1, p,
                reinterpret_cast<uint4*>(p.pairs), count, info);
     if (e != cudaSuccess) return e;
   }
-  const int64_t grid = p.in_order ? chains : std::min<int64_t>(chains * chunks, (int64_t)sms * S::kPerSm);
-  return launch(kernel, (unsigned)grid, kThreads, S::kSmem, stream, init, p);
+  const int64_t grid = p.cluster ? plan.chains * p.cluster : std::min<int64_t>(plan.chains * plan.chunks, kSms * S::kPerSm);
+  e = launch(kernel, (unsigned)grid, kThreads, S::kSmem, stream, init, p.cluster, p);
+  if constexpr (K == kFwd) {
+    if (e == cudaSuccess && a.ckpt)
+      e = launch(scan_save_kernel<IO, RAW, COMPL>,
+                 (unsigned)(div_up(a.D, kBlock) * a.B * div_up(a.T, 4 * S::kR)), 256, 0, stream, true, 1, p);
+  }
+  return e;
 }
 
 }  // namespace
 
-// Enough for every kind of call of these sizes.
+// Enough for every kind of call of these sizes: the header, the words handed
+// between blocks, the rows' information if packed, the forward's states at its
+// units for the checkpoint.
 size_t scan_workspace_bytes(int B, int T, int D, int N, int dtype) {
-  (void)dtype;
   if (B == 0 || T == 0) return 0;
-  size_t words = 0;
-  const auto fit = [&](int width, int rows) {
-    const int64_t chains = (int64_t)B * div_up(D, width), chunks = div_up(T, rows);
-    if (!walked(T, chains)) words = std::max(words, (size_t)(chains * (2 * chunks + div_up(chunks, kGroup)) * width));
+  size_t words = 0, enters = 0;
+  const auto fit = [&](const Plan& q) { words = std::max(words, q.pair_words + q.state_words); };
+  const auto fit_all = [&](auto io) {
+    using IO = decltype(io);
+    const Plan f = plan_for<kFwd, IO, false>(B, T, D);
+    enters = (size_t)(f.chains * f.chunks) * kWarps * Shape<kFwd, IO, false>::W;
+    fit(f), fit(plan_for<kFwd, IO, true>(B, T, D));
+    fit(plan_for<kBwd, IO, false>(B, T, D)), fit(plan_for<kBwd, IO, true>(B, T, D));
+    fit(plan_for<kBwdCkpt, IO, false>(B, T, D));
   };
-  fit(16, 28 * kWarps), fit(16, 60 * kWarps), fit(32, 26 * kWarps), fit(32, 14 * kWarps), fit(128, 28), fit(128, 60);
-  const size_t bytes = words * sizeof(float) + (N > 0 ? align256(((size_t)T + kInfoPad) * 4) : 0);
-  return bytes ? sizeof(WorkspaceHeader) + bytes : 0;
+  if (dtype == KDA_F32)
+    fit_all(float{});
+  else
+    fit_all(__nv_bfloat16{});
+  return sizeof(WorkspaceHeader) + align256(words * 4) + (N > 0 ? info_bytes(T) : 0) + align256(enters * 4);
 }
 
 cudaError_t launch_scan_fwd(const ScanArgs& a, void* ws, cudaStream_t stream) {
   return with_flags(a.dtype, a.prep, a.complement, [&](auto io, auto raw, auto compl_) {
-    return a.ckpt ? launch_tiles<kFwdCkpt, decltype(io), raw.value, compl_.value>(a, ws, stream)
-                  : launch_tiles<kFwd, decltype(io), raw.value, compl_.value>(a, ws, stream);
+    return launch_tiles<kFwd, decltype(io), raw.value, compl_.value>(a, ws, stream);
   });
 }
 

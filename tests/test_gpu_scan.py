@@ -345,6 +345,25 @@ def test_long_sequences(B, T, D, cu, dtype):
     check_backward(got, lam, scan.saved(x, h, s0, complement=True, cu=cu), dh, dsT, True, True, cu)
 
 
+@pytest.mark.parametrize("dtype", DTYPES, ids=DTYPE_IDS)
+@pytest.mark.parametrize("B,T,D,cu", [(5, 500, 1000, None), (1, 2000, 2048, None), (3, 700, 640, None), (20, 600, 300, None),
+                                      (1, 1500, 2600, [0, 1, 480, 700, 1400]), (1, 700, 2501, [5, 699])])
+def test_many_chains(B, T, D, cu, dtype):
+    """Enough sequences and channels that chains are walked by one block, two or four, over several blocks of
+    rows each."""
+    dev = cuda_or_skip()
+    x, g, s0, dh, dsT = make(B, T, D, dtype, True, 115, cu)
+    ckpt = torch.empty(kda_scan_checkpoint_size(B, T, D), dtype=torch.uint8, device=dev)
+    got = kda_scan_fwd(x.to(dev), g.to(dev), s0.to(dev), checkpoint=ckpt, **how(True, True, cu))
+    ref_h, z, E, lam = check_forward(x, g, s0, True, True, cu, got=got)
+    h = torch.from_numpy(ref_h).to(dtype)
+    got = kda_scan_backward(x.to(dev), g.to(dev), h.to(dev), dh.to(dev), s0.to(dev), dsT.to(dev), **how(True, True, cu))
+    check_backward(got, lam, scan.saved(x, h, s0, complement=True, cu=cu), dh, dsT, True, True, cu)
+    lam8, z8 = check_checkpoint(ckpt, x, z, E, lam, True, cu)
+    check_backward(kda_scan_backward_ckpt(ckpt, dh.to(dev), dsT.to(dev), **how(True, True, cu)), lam8, z8, dh, dsT, True,
+                   True, cu)
+
+
 def test_offsets_past_32_bits():
     """2.2e9 elements: the last rows against the oracle over the rows before them (strong gates: what is
     older than 600 rows counts for less than 2^-600), forward, checkpoint and backward."""
