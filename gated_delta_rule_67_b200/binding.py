@@ -40,6 +40,7 @@ SIGNATURES = {
     "kda_backward_ex_workspace_size": (_sz, [_i] * 7),
     "kda_backward_ex": (_i, [_vp] * 5 + [_f] + [_vp] * 9 + [_i] * 8 + [_vp, _sz, _vp]),
     "kda_scan_workspace_size": (_sz, [_i] * 5),
+    "kda_scan_workspace_size_ex": (_sz, [_i] * 6),
     "kda_scan_checkpoint_size": (_sz, [_i] * 3),
     "kda_scan_fwd": (_i, [_vp] * 4 + [_i] + [_vp] * 3 + [_i] * 6 + [_vp, _sz, _vp]),
     "kda_scan_backward": (_i, [_vp] * 7 + [_i] + [_vp] * 3 + [_i] * 6 + [_vp, _sz, _vp]),
@@ -351,8 +352,9 @@ def kda_backward(q, k, v, g, beta, grad_o, scale=None, initial_state=None, grad_
     return out
 
 
-def kda_scan_workspace_size(B, T, D, num_seqs=0, dtype=torch.bfloat16) -> int:
-    return int(load().kda_scan_workspace_size(B, T, D, num_seqs, _dtype_code(dtype)))
+def kda_scan_workspace_size(B, T, D, num_seqs=0, dtype=torch.bfloat16, checkpoint=True) -> int:
+    """Bytes of workspace the scan calls need; less where kda_scan_fwd writes no checkpoint."""
+    return int(load().kda_scan_workspace_size_ex(B, T, D, num_seqs, _dtype_code(dtype), int(checkpoint)))
 
 
 def kda_scan_checkpoint_size(B, T, D) -> int:
@@ -360,57 +362,66 @@ def kda_scan_checkpoint_size(B, T, D) -> int:
     return int(load().kda_scan_checkpoint_size(B, T, D))
 
 
-def _scan_check(device, shape, dtype, cu_seqlens, tensors, states):
-    """Checks what the scan calls share; returns (B, T, D, number of packed sequences).
-    ``tensors``: name -> [B, T, D] tensor, ``states``: name -> fp32 state, either may be None."""
-    if len(shape) != 3:
+# The scan calls are short on the device, so their checks are kept short here: one test of everything, and
+# only where it fails the one that names the fault.
+def _same(name, x, shape, dtype, device):
+    if not (isinstance(x, torch.Tensor) and x.dtype == dtype and x.device == device and x.shape == shape
+            and x.is_contiguous()):
+        _check_dev(name, x, dtype)
+        raise ValueError(f"{name} must be {list(shape)} on {device}, not {list(x.shape)} on {x.device}")
+
+
+def _scan_sizes(x, cu_seqlens):
+    """(B, T, D, number of packed sequences) of the [B, T, D] tensor x."""
+    if x.dim() != 3:
         raise ValueError("the sequence tensors must be [B,T,D]")
-    for name, x in tensors.items():
-        if x is not None:
-            _check_dev(name, x, dtype)
-            if x.shape != shape or x.device != device:
-                raise ValueError(f"{name} must be {list(shape)} on {device}")
-    B, T, D = shape
-    seqs = 0
-    if cu_seqlens is not None:
-        _check_dev("cu_seqlens", cu_seqlens, torch.int32)
-        if cu_seqlens.dim() != 1 or cu_seqlens.numel() < 2 or cu_seqlens.device != device:
-            raise ValueError(f"cu_seqlens must be [num_seqs + 1], num_seqs >= 1, on {device}")
-        if B != 1:
-            raise ValueError("packed sequences (cu_seqlens) need B = 1")
-        seqs = cu_seqlens.numel() - 1
-    for name, x in states.items():
-        if x is not None:
-            _check_dev(name, x, torch.float32)
-            if x.shape != (seqs or B, D) or x.device != device:
-                raise ValueError(f"{name} must be [{seqs or B}, {D}] on {device}")
-    return B, T, D, seqs
+    B, T, D = x.shape
+    if cu_seqlens is None:
+        return B, T, D, 0
+    _check_dev("cu_seqlens", cu_seqlens, torch.int32)
+    if cu_seqlens.dim() != 1 or cu_seqlens.numel() < 2 or cu_seqlens.device != x.device:
+        raise ValueError(f"cu_seqlens must be [num_seqs + 1], num_seqs >= 1, on {x.device}")
+    if B != 1:
+        raise ValueError("packed sequences (cu_seqlens) need B = 1")
+    return B, T, D, cu_seqlens.numel() - 1
 
 
-def _scan_run(name, device, stream, args, shape, code, prep, input_gate, seqs, workspace, made):
-    """Calls a scan entry point with its workspace.  ``made``: the tensors allocated here, which a
-    stream other than the current one must be recorded with."""
-    lib = load()
-    B, T, D = shape
-    need = lib.kda_scan_workspace_size(B, T, D, seqs, code)
-    if workspace is None and need:
-        workspace = torch.empty(need, dtype=torch.uint8, device=device)
-        made.append(workspace)
-    elif workspace is not None:
-        _check_dev("workspace", workspace)
-    nbytes = 0 if workspace is None else workspace.numel() * workspace.element_size()
-    with _on(device):
-        st = getattr(lib, name)(*args, B, T, D, code, int(prep), int(input_gate), _ptr(workspace), nbytes,
-                                _stream(stream, device))
-    _record(made, stream, device)
+def _at(x):
+    return None if x is None else x.data_ptr()
+
+
+def _scan_call(name, device, stream, args, made):
+    """One call of the library on the device's stream.  ``made``: the tensors allocated here, which a stream
+    other than the current one must be recorded with."""
+    fn = getattr(load(), name)
+    index = device.index
+    current = torch._C._cuda_getCurrentRawStream(index)
+    raw = current if stream is None else stream.cuda_stream
+    if torch.cuda.current_device() == index:
+        st = fn(*args, raw)
+    else:
+        with _on(device):
+            st = fn(*args, raw)
+    if raw != current:
+        for t in made:
+            t.record_stream(stream)
     if st != KDA_OK:
         raise KDAError(st, name)
 
 
-def _record(made, stream, device):
-    if stream is not None and stream != torch.cuda.current_stream(device):
-        for t in made:
-            t.record_stream(stream)
+def _scan_workspace(workspace, x, B, T, D, seqs, code, checkpoint, made):
+    """(address, bytes) of the caller's workspace or of one made here."""
+    if workspace is None:
+        need = load().kda_scan_workspace_size_ex(B, T, D, seqs, code, checkpoint)
+        if not need:
+            return None, 0
+        workspace = torch.empty(need, dtype=torch.uint8, device=x.device)
+        made.append(workspace)
+    else:
+        _check_dev("workspace", workspace)
+        if workspace.device != x.device:
+            raise ValueError(f"workspace must live on {x.device}")
+    return workspace.data_ptr(), workspace.numel() * workspace.element_size()
 
 
 def kda_scan_fwd(x, g, initial_state=None, *, cu_seqlens=None, input_gate=KDA_SCAN_INPUT_PLAIN, prep=0, h=None,
@@ -427,21 +438,29 @@ def kda_scan_fwd(x, g, initial_state=None, *, cu_seqlens=None, input_gate=KDA_SC
     ``initial_state`` itself.
     """
     _check_dev("x", x)
-    code = _dtype_code(x.dtype)
-    B, T, D, seqs = _scan_check(x.device, x.shape, x.dtype, cu_seqlens, {"g": g, "h": h},
-                                {"initial_state": initial_state, "final_state": final_state})
-    if checkpoint is not None:
-        _check_ckpt(checkpoint, x.shape, x.device)
+    device, dtype, code = x.device, x.dtype, _dtype_code(x.dtype)
+    B, T, D, seqs = _scan_sizes(x, cu_seqlens)
+    state = (seqs or B, D)
+    _same("g", g, x.shape, dtype, device)
+    if initial_state is not None:
+        _same("initial_state", initial_state, state, torch.float32, device)
     made = []
     if h is None:
         h = torch.empty_like(x)
         made.append(h)
-    if final_state is None and output_final_state:
-        final_state = torch.empty((seqs or B, D), dtype=torch.float32, device=x.device)
+    else:
+        _same("h", h, x.shape, dtype, device)
+    if final_state is not None:
+        _same("final_state", final_state, state, torch.float32, device)
+    elif output_final_state:
+        final_state = torch.empty(state, dtype=torch.float32, device=device)
         made.append(final_state)
-    args = (_ptr(x), _ptr(g), _ptr(initial_state), _ptr(cu_seqlens), seqs, _ptr(h), _ptr(final_state),
-            _ptr(checkpoint))
-    _scan_run("kda_scan_fwd", x.device, stream, args, (B, T, D), code, prep, input_gate, seqs, workspace, made)
+    if checkpoint is not None:
+        _check_ckpt(checkpoint, x.shape, device)
+    ws, nbytes = _scan_workspace(workspace, x, B, T, D, seqs, code, checkpoint is not None, made)
+    _scan_call("kda_scan_fwd", device, stream,
+               (x.data_ptr(), g.data_ptr(), _at(initial_state), _at(cu_seqlens), seqs, h.data_ptr(), _at(final_state),
+                _at(checkpoint), B, T, D, code, prep, input_gate, ws, nbytes), made)
     return h, final_state
 
 
@@ -452,10 +471,10 @@ def _check_ckpt(checkpoint, shape, device):
         raise ValueError(f"checkpoint must hold {need} bytes on {device}")
 
 
-def _scan_grads(like, seqs, want_initial_state_grad, made):
+def _scan_grads(like, state, want_initial_state_grad, made):
     out = dict(dx=torch.empty_like(like), dg=torch.empty_like(like), dS0=None)
     if want_initial_state_grad:
-        out["dS0"] = torch.empty((seqs or like.shape[0], like.shape[2]), dtype=torch.float32, device=like.device)
+        out["dS0"] = torch.empty(state, dtype=torch.float32, device=like.device)
     made.extend(t for t in out.values() if t is not None)
     return out
 
@@ -468,16 +487,26 @@ def kda_scan_backward(x, g, h, grad_h, initial_state=None, grad_final_state=None
     KDA_SCAN_INPUT_PLAIN.  Returns a dict: dx, dg (input dtype) and dS0 fp32 (None if not wanted).
     """
     _check_dev("grad_h", grad_h)
-    code = _dtype_code(grad_h.dtype)
-    if input_gate == KDA_SCAN_INPUT_COMPLEMENT and x is None:
+    device, dtype, code = grad_h.device, grad_h.dtype, _dtype_code(grad_h.dtype)
+    B, T, D, seqs = _scan_sizes(grad_h, cu_seqlens)
+    state = (seqs or B, D)
+    if x is not None:
+        _same("x", x, grad_h.shape, dtype, device)
+    elif input_gate == KDA_SCAN_INPUT_COMPLEMENT:
         raise ValueError("x is needed for KDA_SCAN_INPUT_COMPLEMENT")
-    B, T, D, seqs = _scan_check(grad_h.device, grad_h.shape, grad_h.dtype, cu_seqlens, {"x": x, "g": g, "h": h},
-                                {"initial_state": initial_state, "grad_final_state": grad_final_state})
+    _same("g", g, grad_h.shape, dtype, device)
+    _same("h", h, grad_h.shape, dtype, device)
+    if initial_state is not None:
+        _same("initial_state", initial_state, state, torch.float32, device)
+    if grad_final_state is not None:
+        _same("grad_final_state", grad_final_state, state, torch.float32, device)
     made = []
-    out = _scan_grads(grad_h, seqs, want_initial_state_grad, made)
-    args = (_ptr(x), _ptr(g), _ptr(h), _ptr(initial_state), _ptr(grad_h), _ptr(grad_final_state), _ptr(cu_seqlens),
-            seqs, _ptr(out["dx"]), _ptr(out["dg"]), _ptr(out["dS0"]))
-    _scan_run("kda_scan_backward", grad_h.device, stream, args, (B, T, D), code, prep, input_gate, seqs, workspace, made)
+    out = _scan_grads(grad_h, state, want_initial_state_grad, made)
+    ws, nbytes = _scan_workspace(workspace, grad_h, B, T, D, seqs, code, 0, made)
+    _scan_call("kda_scan_backward", device, stream,
+               (_at(x), g.data_ptr(), h.data_ptr(), _at(initial_state), grad_h.data_ptr(), _at(grad_final_state),
+                _at(cu_seqlens), seqs, out["dx"].data_ptr(), out["dg"].data_ptr(), _at(out["dS0"]), B, T, D, code, prep,
+                input_gate, ws, nbytes), made)
     return out
 
 
@@ -487,16 +516,19 @@ def kda_scan_backward_ckpt(checkpoint, grad_h, grad_final_state=None, *, cu_seql
     """kda_scan_backward from the 8-bit checkpoint that kda_scan_fwd filled (same sizes, ``prep``, ``input_gate``
     and ``cu_seqlens``) in place of x, g, h and the initial state."""
     _check_dev("grad_h", grad_h)
-    code = _dtype_code(grad_h.dtype)
-    B, T, D, seqs = _scan_check(grad_h.device, grad_h.shape, grad_h.dtype, cu_seqlens, {},
-                                {"grad_final_state": grad_final_state})
-    _check_ckpt(checkpoint, grad_h.shape, grad_h.device)
+    device, code = grad_h.device, _dtype_code(grad_h.dtype)
+    B, T, D, seqs = _scan_sizes(grad_h, cu_seqlens)
+    state = (seqs or B, D)
+    if grad_final_state is not None:
+        _same("grad_final_state", grad_final_state, state, torch.float32, device)
+    _check_ckpt(checkpoint, grad_h.shape, device)
     made = []
-    out = _scan_grads(grad_h, seqs, want_initial_state_grad, made)
-    args = (_ptr(checkpoint), _ptr(grad_h), _ptr(grad_final_state), _ptr(cu_seqlens), seqs, _ptr(out["dx"]),
-            _ptr(out["dg"]), _ptr(out["dS0"]))
-    _scan_run("kda_scan_backward_ckpt", grad_h.device, stream, args, (B, T, D), code, prep, input_gate, seqs, workspace,
-              made)
+    out = _scan_grads(grad_h, state, want_initial_state_grad, made)
+    ws, nbytes = _scan_workspace(workspace, grad_h, B, T, D, seqs, code, 0, made)
+    _scan_call("kda_scan_backward_ckpt", device, stream,
+               (checkpoint.data_ptr(), grad_h.data_ptr(), _at(grad_final_state), _at(cu_seqlens), seqs,
+                out["dx"].data_ptr(), out["dg"].data_ptr(), _at(out["dS0"]), B, T, D, code, prep, input_gate, ws,
+                nbytes), made)
     return out
 
 
@@ -504,23 +536,22 @@ def kda_scan_step(x, g, state, *, input_gate=KDA_SCAN_INPUT_PLAIN, prep=0, h=Non
     """One token of the elementwise recurrence for N sequences: x, g [N,D], state [N,D] fp32, updated in place, or
     left and the new one written to ``out_state``.  Returns h [N,D] in the input dtype."""
     _check_dev("x", x)
-    code = _dtype_code(x.dtype)
+    device, code = x.device, _dtype_code(x.dtype)
     if x.dim() != 2:
         raise ValueError("x must be [N,D]")
-    out_state = state if out_state is None else out_state
     made = []
     if h is None:
         h = torch.empty_like(x)
         made.append(h)
-    for name, t, dtype in (("g", g, x.dtype), ("state", state, torch.float32), ("out_state", out_state, torch.float32),
-                           ("h", h, x.dtype)):
-        _check_dev(name, t, dtype)
-        if t.shape != x.shape or t.device != x.device:
-            raise ValueError(f"{name} must be {list(x.shape)} on {x.device}")
-    with _on(x.device):
-        st = load().kda_scan_step(_ptr(x), _ptr(g), _ptr(state), _ptr(out_state), _ptr(h), x.shape[0], x.shape[1],
-                                  code, int(prep), int(input_gate), _stream(stream, x.device))
-    _record(made, stream, x.device)
-    if st != KDA_OK:
-        raise KDAError(st, "kda_scan_step")
+    else:
+        _same("h", h, x.shape, x.dtype, device)
+    _same("g", g, x.shape, x.dtype, device)
+    _same("state", state, x.shape, torch.float32, device)
+    if out_state is None:
+        out_state = state
+    else:
+        _same("out_state", out_state, x.shape, torch.float32, device)
+    _scan_call("kda_scan_step", device, stream,
+               (x.data_ptr(), g.data_ptr(), state.data_ptr(), out_state.data_ptr(), h.data_ptr(), x.shape[0], x.shape[1],
+                code, prep, input_gate), made)
     return h

@@ -332,9 +332,13 @@ static kda_status scan_sizes(int64_t B, int64_t T, int64_t D, int64_t N, int dty
   return KDA_OK;
 }
 
-size_t kda_scan_workspace_size(int B, int T, int D, int num_seqs, int dtype) {
+size_t kda_scan_workspace_size_ex(int B, int T, int D, int num_seqs, int dtype, int checkpoint) {
   if (scan_sizes(B, T, D, num_seqs, dtype) != KDA_OK || (num_seqs > 0 && B != 1)) return 0;
-  return kda::scan_workspace_bytes(B, T, D, num_seqs, dtype);
+  return kda::scan_workspace_bytes(B, T, D, num_seqs, dtype, checkpoint != 0);
+}
+
+size_t kda_scan_workspace_size(int B, int T, int D, int num_seqs, int dtype) {
+  return kda_scan_workspace_size_ex(B, T, D, num_seqs, dtype, 0);
 }
 
 size_t kda_scan_checkpoint_size(int B, int T, int D) {
@@ -361,7 +365,8 @@ static kda_status scan_checks(const kda::ScanArgs& a, const Range* in, int n_in,
     for (int j = i + 1; j < n_out; ++j)
       if (overlaps(out[i], out[j])) return KDA_ERR_INVALID_ARG;
   }
-  const size_t need_ws = kda::scan_workspace_bytes(a.B, a.T, a.D, a.N, a.dtype);
+  // the checkpoint is written (by the forward: it has no dy) from states kept in the workspace
+  const size_t need_ws = kda::scan_workspace_bytes(a.B, a.T, a.D, a.N, a.dtype, a.ckpt && !a.dy);
   if (need_ws) {
     if (!workspace || workspace_bytes < need_ws || (reinterpret_cast<uintptr_t>(workspace) & 255u))
       return KDA_ERR_INVALID_ARG;
@@ -372,6 +377,11 @@ static kda_status scan_checks(const kda::ScanArgs& a, const Range* in, int n_in,
       if (overlaps(rw, out[i])) return KDA_ERR_INVALID_ARG;
   }
   return KDA_OK;
+}
+
+// The workspace of a call that needs one, else null (nothing is written to a buffer it does not need).
+static void* scan_workspace(const kda::ScanArgs& a, void* workspace) {
+  return kda::scan_workspace_bytes(a.B, a.T, a.D, a.N, a.dtype, a.ckpt && !a.dy) ? workspace : nullptr;
 }
 
 static kda_status scan_flags(int64_t B, int64_t T, int64_t D, const int32_t* cu, int64_t num_seqs, int dtype, int prep,
@@ -411,7 +421,7 @@ kda_status kda_scan_fwd(const void* x, const void* g, const float* initial_state
   st = scan_checks(a, in, 4, out, 3, need, 3, workspace, workspace_bytes);
   if (st != KDA_OK) return st;
   if (B == 0 || T == 0) return scan_empty(initial_state, final_state, sb, stream);
-  return from_cuda(kda::launch_scan_fwd(a, workspace, stream));
+  return from_cuda(kda::launch_scan_fwd(a, scan_workspace(a, workspace), stream));
 }
 
 kda_status kda_scan_backward(const void* x, const void* g, const void* h, const float* initial_state,
@@ -438,7 +448,7 @@ kda_status kda_scan_backward(const void* x, const void* g, const void* h, const 
   st = scan_checks(a, in, 7, out, 3, need, 6, workspace, workspace_bytes);
   if (st != KDA_OK) return st;
   if (B == 0 || T == 0) return scan_empty(grad_final_state, grad_initial_state, sb, stream);
-  return from_cuda(kda::launch_scan_bwd(a, workspace, stream));
+  return from_cuda(kda::launch_scan_bwd(a, scan_workspace(a, workspace), stream));
 }
 
 kda_status kda_scan_backward_ckpt(const void* checkpoint, const void* grad_h, const float* grad_final_state,
@@ -462,7 +472,7 @@ kda_status kda_scan_backward_ckpt(const void* checkpoint, const void* grad_h, co
   st = scan_checks(a, in, 4, out, 3, need, 4, workspace, workspace_bytes);
   if (st != KDA_OK) return st;
   if (B == 0 || T == 0) return scan_empty(grad_final_state, grad_initial_state, sb, stream);
-  return from_cuda(kda::launch_scan_bwd(a, workspace, stream));
+  return from_cuda(kda::launch_scan_bwd(a, scan_workspace(a, workspace), stream));
 }
 
 kda_status kda_scan_step(const void* x, const void* g, const float* state, float* out_state, void* h, int N, int D,

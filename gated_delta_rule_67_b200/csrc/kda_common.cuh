@@ -142,7 +142,7 @@ inline __host__ __device__ ScanCkptLayout scan_ckpt_layout(size_t rows, int D) {
   l.total = 2 * (codes + scales);
   return l;
 }
-size_t scan_workspace_bytes(int B, int T, int D, int N, int dtype);
+size_t scan_workspace_bytes(int B, int T, int D, int N, int dtype, bool checkpoint);
 cudaError_t launch_scan_fwd(const ScanArgs& a, void* ws, cudaStream_t stream);
 cudaError_t launch_scan_bwd(const ScanArgs& a, void* ws, cudaStream_t stream);
 cudaError_t launch_scan_step(const void* x, const void* g, const float* state, float* out_state, void* h, size_t n,

@@ -62,6 +62,7 @@ constexpr int kThreads = 32 * kWarps;
 constexpr int kGroup = 16;      // few chains: tiles from one published state to the next
 constexpr int kCluster = 8;     // blocks that walk a chain together, at most
 constexpr int kJoinChains = 16; // fewer chains, of more than
+constexpr int kWideChains = 128;  // chains of 64 channels from which the backward from the checkpoint takes them
 constexpr int kJoinTiles = 32;  // so many tiles each, are joined tile by tile
 constexpr int kInfoPad = 512;   // rows of padding behind the packed sequences' row information
 constexpr uint32_t kEmpty = 0xffffffffu;     // a word not yet written
@@ -185,12 +186,6 @@ __device__ __forceinline__ uint32_t magnitude(float v) {  // for the block's max
   return b < 0x7f800000u ? b : 0u;
 }
 __device__ __forceinline__ bool finite(float v) { return fabsf(v) <= 3.402823466e38f; }
-// Two values as e4m3 of v * inv (inv a power of two; non-finite values give NaN).
-__device__ __forceinline__ uint16_t encode2(const float* v, float inv) {
-  const float a = finite(v[0]) ? v[0] * inv : __int_as_float(0x7fffffff);
-  const float b = finite(v[1]) ? v[1] * inv : __int_as_float(0x7fffffff);
-  return __nv_cvt_float2_to_fp8x2(make_float2(a, b), __NV_SATFINITE, __NV_E4M3);
-}
 __device__ __forceinline__ float2 decode2(uint16_t c) { return __half22float2(__half2(__nv_cvt_fp8x2_to_halfraw2(c, __NV_E4M3))); }
 
 // ----------------------------------------------- V = 2 or 4 channels of a row
@@ -323,26 +318,29 @@ __device__ __forceinline__ uint32_t peek(const float* p) {
 }
 
 // ------------------------------------------------------------------ the tiles
-enum Kind { kFwd, kBwd, kBwdCkpt };
+enum Kind { kFwd, kBwd, kBwdCkpt, kBwdCkptNarrow };
 
 // Tiles.  A thread holds two channels x one segment of kR rows; kR is odd, so
 // that the segments side by side in a warp lie in different banks, and as
 // large as registers and the stages of two blocks in an SM's shared memory
-// allow.  Rows are 64 bytes of bf16 or fp32; 128 from the checkpoint, whose
-// codes are one byte.
+// allow.  Rows are 64 bytes of bf16 or fp32.  From the checkpoint, whose codes
+// are one byte, 64 channels are best for bf16 where the chains are many (143
+// us against 163 with 32 at B8 T4096 D2048), 32 where they are few (32767 packed
+// rows of 1024 channels, forward and backward: 324 us against 396); fp32 takes 32.
 template <Kind K, typename IO, bool COMPL>
 struct Shape {
   static constexpr bool kDown = K != kFwd;
-  static constexpr int W = sizeof(IO) == 4 ? (K == kBwdCkpt ? 32 : 16) : K == kBwdCkpt ? 64 : 32;
+  static constexpr bool kFrom = K == kBwdCkpt || K == kBwdCkptNarrow;
+  static constexpr int W = K == kBwdCkpt ? 64 : sizeof(IO) == 4 && !kFrom ? 16 : 32;
   static constexpr int kCh = W > 32 ? 2 : 1;                       // channels of a lane on the ways between levels
-  static constexpr int kR = sizeof(IO) == 4 || K == kBwd ? 7 : K == kBwdCkpt ? 13 : 15;
+  static constexpr int kR = sizeof(IO) == 4 || K == kBwd ? 7 : K == kBwdCkpt ? 13 : kFrom ? 11 : 15;
   static constexpr int kAcross = W / 2;                            // threads of a row
   static constexpr int kSide = 32 / kAcross;                       // segments of a unit
   static constexpr int kUnitRows = kSide * kR, kL = kWarps * kUnitRows;
-  static constexpr int kBox = kL <= 256 ? kL : kL / 2;             // rows of one TMA load
+  static_assert(kL <= 256, "a tile's input is one TMA box");
   // input arrays: forward x, g; backward dy, g, h, x; from the checkpoint dy, lambda, z
-  static constexpr int kIn = K == kBwd ? (COMPL ? 4 : 3) : K == kBwdCkpt ? 3 : 2;
-  __host__ __device__ static constexpr int eb(int i) { return K == kBwdCkpt && i > 0 ? 1 : (int)sizeof(IO); }
+  static constexpr int kIn = K == kBwd ? (COMPL ? 4 : 3) : kFrom ? 3 : 2;
+  __host__ __device__ static constexpr int eb(int i) { return kFrom && i > 0 ? 1 : (int)sizeof(IO); }
   __host__ __device__ static constexpr int at(int i) {
     int o = 0;
     for (int j = 0; j < i; ++j) o += kL * W * eb(j);
@@ -350,7 +348,7 @@ struct Shape {
   }
   static constexpr int kStage = at(kIn), kStages = 3;
   // the backward's dL/dg takes the place of g, or, for want of it, a buffer of its own behind the stages
-  static constexpr int kOwn = K == kBwdCkpt ? kL * W * (int)sizeof(IO) : 0;
+  static constexpr int kOwn = kFrom ? kL * W * (int)sizeof(IO) : 0;
   static constexpr int kSmem = kStages * kStage + kOwn;
   static constexpr int kPerSm = kSmem > 98304 ? 1 : 2;
   static_assert(kStage % 128 == 0 && kUnitRows * W * sizeof(IO) % 128 == 0, "TMA needs 128-byte places");
@@ -363,7 +361,7 @@ struct TileArgs {
   WorkspaceHeader* hdr;     // error word; pad[0] is the ticket
   float* pairs;             // kJoin: [chains][chunks][2][W]
   float* states;            // kJoin: [chains][groups][W]
-  float* enters;            // with a checkpoint: [chains][chunks * kWarps][W], what enters each unit, else null
+  float* enters;            // with a checkpoint: [chains][segments][W], what enters each segment, else null
   const int32_t* info;      // packed: sequence * 4 + first * 2 + last of each row, -1 outside
   int chains, chunks, groups, blocks;  // blocks: of channels
   int cluster;              // blocks that walk a chain; 0: kJoin
@@ -395,7 +393,7 @@ __global__ void __launch_bounds__(kThreads, Shape<K, IO, COMPL>::kPerSm)
     scan_tile_kernel(const __grid_constant__ TileArgs p) {
   using S = Shape<K, IO, COMPL>;
   constexpr int W = S::W, R = S::kR, L = S::kL, NS = S::kStages;
-  constexpr bool kDown = S::kDown, kFrom = K == kBwdCkpt;
+  constexpr bool kDown = S::kDown, kFrom = S::kFrom;
   extern __shared__ __align__(128) uint8_t stages[];
   __shared__ Shared<S> sh;
   const ScanArgs& a = p.a;
@@ -409,6 +407,8 @@ __global__ void __launch_bounds__(kThreads, Shape<K, IO, COMPL>::kPerSm)
     for (int s = 0; s < NS; ++s) mbar_init(&sh.full[s], 1);
     for (int s = 0; s < 2; ++s) mbar_init(&sh.came[s], 1);
     fence_mbar_init();
+    for (int i = 0; i < S::kIn; ++i)
+      if (p.tma || (kFrom && i > 0)) prefetch_tensormap(&p.map[i]);
   }
   const bool walk = p.cluster > 0;
   const uint32_t size = walk ? p.cluster : 1, rank = walk ? blockIdx.x % size : 0;
@@ -441,31 +441,61 @@ __global__ void __launch_bounds__(kThreads, Shape<K, IO, COMPL>::kPerSm)
   };
   auto chain_of = [&](const Place& q) { return (size_t)q.b * p.blocks + q.cb; };
   const ScanCkptLayout lay = scan_ckpt_layout(rows, a.D);
-  auto scale_at = [&](const Place& q) { return (size_t)(q.cb * W / kBlock) * rows + (size_t)q.b * a.T + q.t0; };
+  auto scale_at = [&](int b, int cb, int t0) { return (size_t)(cb * W / kBlock) * rows + (size_t)b * a.T + t0; };
 
-  // ---- thread 0: the tiles of this block one after the other
+  // ---- thread 0: the tiles of this block one after the other.  Kept short: warp 0 does this beside its rows,
+  // and every warp waits for the last.
   uint32_t drawn = 0;  // kJoin: the next ticket
-  const int my_chain = (int)(blockIdx.x / size);
-  int4 next = make_int4(0, (int)rank - (int)size, my_chain / p.blocks, my_chain % p.blocks);
-  if (threadIdx.x == 0 && !walk) next.y = 0, drawn = atomicAdd(&p.hdr->pad[0], 1u);
-  bool more = true;
-  auto advance = [&]() {
-    if (!more) return next;
-    if (walk) {
-      next.y += size;
-      more = next.y < p.chunks;
-    } else {
-      more = drawn < (uint32_t)p.chains * (uint32_t)p.chunks;
-      if (more) {
-        const int chain = (int)(drawn % (uint32_t)p.chains);
-        next.y = (int)(drawn / (uint32_t)p.chains);
-        next.z = chain / p.blocks, next.w = chain % p.blocks;
-        drawn = atomicAdd(&p.hdr->pad[0], 1u);
-      }
-    }
-    if (!more) next.y = -1;
+  const int my_chain = (int)(blockIdx.x / size), stride = (kDown ? -L : L) * (int)size;
+  int4 next = make_int4((kDown ? (p.chunks - 1 - (int)rank) * L : (int)rank * L), (int)rank, my_chain / p.blocks,
+                        my_chain % p.blocks);
+  int slot = 0;        // the stage of the next tile
+  auto draw = [&]() {  // kJoin
+    const bool there = drawn < (uint32_t)p.chains * (uint32_t)p.chunks;
+    const int chain = (int)(drawn % (uint32_t)p.chains);
+    next.y = there ? (int)(drawn / (uint32_t)p.chains) : p.chunks;
+    next.z = chain / p.blocks, next.w = chain % p.blocks;
     next.x = (kDown ? p.chunks - 1 - next.y : next.y) * L;
-    return next;
+    if (there) drawn = atomicAdd(&p.hdr->pad[0], 1u);
+  };
+  if (threadIdx.x == 0 && !walk) drawn = atomicAdd(&p.hdr->pad[0], 1u), draw();
+  // the next one into its stage
+  auto feed = [&]() {
+    uint64_t* bar = &sh.full[slot];
+    if (next.y >= p.chunks) {
+      sh.tile[slot].y = -1;
+      mbar_arrive(bar);
+    } else {
+      sh.tile[slot] = next;
+      uint8_t* st = stages + slot * S::kStage;
+      constexpr uint32_t kArray = L * W * sizeof(IO);  // an array in the caller's type
+      uint32_t bytes = (p.tma ? (kFrom ? 1 : S::kIn) * kArray : 0) + (kFrom ? 2 * L * W : 0) + (packed ? L * 4 : 0);
+      uint32_t scale_bytes = 0;
+      size_t at = 0;
+      if (kFrom) {
+        at = scale_at(next.z, next.w, next.x);
+        scale_bytes = ((uint32_t)(at & 15) + (uint32_t)min(L, a.T - next.x) + 15) & ~15u;
+        bytes += 2 * scale_bytes;
+      }
+      if (bytes)
+        mbar_expect_tx(bar, bytes);
+      else
+        mbar_arrive(bar);
+#pragma unroll
+      for (int i = 0; i < S::kIn; ++i)
+        if (p.tma || (kFrom && i > 0))  // h one row up: what enters each row
+          tma_load_3d(st + S::at(i), &p.map[i], bar, next.w * W, next.x - (K == kBwd && i == 2 ? 1 : 0), next.z);
+      if (packed) bulk_load(sh.info[slot], p.info + next.x, L * 4, bar);
+      if (kFrom) {
+        bulk_load(sh.scale[slot][0], a.ckpt + lay.lam_scale + (at & ~size_t(15)), scale_bytes, bar);
+        bulk_load(sh.scale[slot][1], a.ckpt + lay.z_scale + (at & ~size_t(15)), scale_bytes, bar);
+      }
+      if (walk)
+        next.y += size, next.x += stride;
+      else
+        draw();
+    }
+    slot = slot == NS - 1 ? 0 : slot + 1;
   };
   // walk: the barrier of the k-th tile's state; the chain's first tile has none.  A block that walks alone
   // writes its own state and arrives by itself.
@@ -475,43 +505,8 @@ __global__ void __launch_bounds__(kThreads, Shape<K, IO, COMPL>::kPerSm)
     else if (size > 1)
       mbar_expect_tx(&sh.came[k & 1], W * 4);
   };
-  // ---- thread 0: the k-th tile into its stage
-  auto feed = [&](int k, int4 tile) {
-    const int s = k % NS;
-    sh.tile[s] = tile;
-    if (tile.y < 0) {
-      mbar_arrive(&sh.full[s]);
-      return;
-    }
-    const Place q = place_of(k, tile);
-    constexpr uint32_t kArray = L * W * sizeof(IO);  // an array in the caller's type
-    uint32_t bytes = (p.tma ? (kFrom ? 1 : S::kIn) * kArray : 0) + (kFrom ? 2 * L * W : 0) + (packed ? L * 4 : 0);
-    uint32_t scale_bytes = 0;
-    if (kFrom) {
-      scale_bytes = ((uint32_t)(scale_at(q) & 15) + (uint32_t)min(L, a.T - q.t0) + 15) & ~15u;
-      bytes += 2 * scale_bytes;
-    }
-    if (bytes)
-      mbar_expect_tx(&sh.full[s], bytes);
-    else
-      mbar_arrive(&sh.full[s]);
-#pragma unroll
-    for (int i = 0; i < S::kIn; ++i)
-      if (p.tma || (kFrom && i > 0))
-#pragma unroll
-        for (int part = 0; part < L / S::kBox; ++part)  // h one row up: what enters each row
-          tma_load_3d(q.st + S::at(i) + part * S::kBox * W * S::eb(i), &p.map[i], &sh.full[s], q.cb * W,
-                      q.t0 + part * S::kBox - (K == kBwd && i == 2 ? 1 : 0), q.b);
-    if (packed) bulk_load(sh.info[s], p.info + q.t0, L * 4, &sh.full[s]);
-    if (kFrom) {
-      const size_t at = scale_at(q) & ~size_t(15);
-      bulk_load(sh.scale[s][0], a.ckpt + lay.lam_scale + at, scale_bytes, &sh.full[s]);
-      bulk_load(sh.scale[s][1], a.ckpt + lay.z_scale + at, scale_bytes, &sh.full[s]);
-    }
-  };
   if (threadIdx.x == 0) {
-    feed(0, advance()), feed(1, advance());
-    advance();
+    feed(), feed();
     if (walk) expect(0, rank == 0), expect(1, false);
   }
 
@@ -596,7 +591,7 @@ __global__ void __launch_bounds__(kThreads, Shape<K, IO, COMPL>::kPerSm)
     }
     const Place q = place_of(k, tile);
     // rows out of the ordinary: none in most tiles
-    const bool edge = has_edge(q) || !p.tma;
+    const bool edge = has_edge(q);
     float2(*pair)[W] = sh.pair[k & 1];
     constexpr int kCh = S::kCh;
     const int ch = kCh * lane % W;  // on the ways between segment, unit and tile; with 16 channels half of a warp repeats the other
@@ -614,13 +609,24 @@ __global__ void __launch_bounds__(kThreads, Shape<K, IO, COMPL>::kPerSm)
     };
     if constexpr (kFrom) {
       if (lane < S::kUnitRows) {
-        const int off = (int)(scale_at(q) & 15) + lowest + lane;
+        const int off = (int)(scale_at(q.b, q.cb, q.t0) & 15) + lowest + lane;
         sh.scale_of[warp][0][lane] = pow2(sh.scale[q.s][0][off]);
         sh.scale_of[warp][1][lane] = pow2(sh.scale[q.s][1][off]);
       }
       __syncwarp();
     }
 
+    // bit r: whether this thread's row r belongs to a sequence, is where the recurrence starts, and ends
+    uint32_t valid = 0, start = 0, stop = 0;
+    if (edge) {
+#pragma unroll 1
+      for (int r = 0; r < R; ++r) {
+        const Row o = row_info(q, row_at(r));
+        valid |= (uint32_t)o.valid << r;
+        start |= (uint32_t)(o.valid && (kDown ? o.last : o.first)) << r;
+        stop |= (uint32_t)(o.valid && (kDown ? o.first : o.last)) << r;
+      }
+    }
     // ---- segments as pairs
     f2 al[R], in[R];  // alpha; forward: the input, backward: 1 - alpha
     auto reduce = [&](auto edges) {
@@ -635,10 +641,9 @@ __global__ void __launch_bounds__(kThreads, Shape<K, IO, COMPL>::kPerSm)
         const f2 x = load2(q, 0, i);
         gate<RAW && !kFrom>(g, al[r], be);
         in[r] = kDown ? be : COMPL ? mul2(be, x) : x;
-        const Row o = E ? row_info(q, i) : Row{true, false, false, 0};
-        if (E && !o.valid) continue;
-        if (E && (kDown ? o.last : o.first)) {
-          const f2 f = state_of(q, a.s0, o.seq);
+        if (E && !(valid >> r & 1)) continue;
+        if (E && (start >> r & 1)) {
+          const f2 f = state_of(q, a.s0, row_info(q, i).seq);
           if (!kDown) in[r] = fma2(al[r], f, in[r]);
           A = both(-0.f);
           B = kDown ? mul2(al[r], add2(x, f)) : in[r];
@@ -670,7 +675,7 @@ __global__ void __launch_bounds__(kThreads, Shape<K, IO, COMPL>::kPerSm)
     __syncthreads();  // the pairs are there, and every warp is done with the tile before
     if (threadIdx.x == 0) {
       if (walk && k > 0) expect(k + 1, false);
-      feed(k + 2, next);  // into its stage
+      feed();  // into its stage
     }
 
     // ---- what enters the tile
@@ -746,19 +751,18 @@ __global__ void __launch_bounds__(kThreads, Shape<K, IO, COMPL>::kPerSm)
       for (int j = 0; j < kCh; ++j) e[j] = sh.into[warp][ch + j];
     }
 
-    // ---- what enters the unit, then this thread's segment
-    if (K == kFwd && p.enters) {
-#pragma unroll
-      for (int j = 0; j < kCh; ++j)
-        p.enters[((chain_of(q) * p.chunks + q.chunk) * kWarps + warp) * W + ch + j] = e[j];
-    }
+    // ---- what enters this thread's segment
     f2 h;  // forward: the state, backward: c_{t+1}
     if constexpr (S::kSide == 1) {
       h = pack(e[0], e[kCh - 1]);
     } else {
+      float* keep = nullptr;
+      if (K == kFwd && p.enters)
+        keep = p.enters + ((chain_of(q) * p.chunks + q.chunk) * kWarps + warp) * (S::kSide * W) + ch;
 #pragma unroll
       for (int g = 0; g < S::kSide; ++g) {
         sh.enter[warp][g][ch] = e[0];
+        if (K == kFwd && keep) keep[g * W] = e[0];
         e[0] = through(e[0], sg[g]);
       }
       __syncwarp();
@@ -779,51 +783,54 @@ __global__ void __launch_bounds__(kThreads, Shape<K, IO, COMPL>::kPerSm)
       else
         put<IO>(place, w[0], w[1]);
     };
-    auto emit = [&](auto edges) {
+    auto emit = [&](auto edges, auto pitched) {
       constexpr bool E = decltype(edges)::value;
-      const bool direct = E && !p.tma;
+      const bool direct = E ? !p.tma : !decltype(pitched)::value;
 #pragma unroll
       for (int r = 0; r < R; ++r) {
         const int i = row_at(r);
-        const Row o = E ? row_info(q, i) : Row{true, false, false, 0};
-        if (E && !o.valid) {  // past the end, or a row that no sequence owns
+        if (E && !(valid >> r & 1)) {  // past the end, or a row that no sequence owns
           if (!direct || q.t0 + i < a.T) {
             store(static_cast<IO*>(a.out), elem(q, 0, i), i, both(0.f), direct);
             if (kDown) store(static_cast<IO*>(a.dg), second(i), i, both(0.f), direct);
           }
           continue;
         }
-        const bool start = E && (kDown ? o.last : o.first);
+        const bool starts = E && (start >> r & 1);
         if constexpr (!kDown) {
-          h = start ? in[r] : fma2(al[r], h, in[r]);
+          h = starts ? in[r] : fma2(al[r], h, in[r]);
           store(static_cast<IO*>(a.out), elem(q, 0, i), i, h, direct);
         } else {
           f2 z;
           if constexpr (kFrom) z = codes_of(q, 2, i);
           else {
-            z = E && o.first ? state_of(q, a.h0, o.seq) : load2(q, 2, i);
+            z = E && (stop >> r & 1) ? state_of(q, a.h0, row_info(q, i).seq) : load2(q, 2, i);
             if (COMPL) z = add2(z, neg2(load2(q, 3, i)));
           }
-          const f2 d = add2(load2(q, 0, i), start ? state_of(q, a.s0, o.seq) : h);
+          const f2 d = add2(load2(q, 0, i), starts ? state_of(q, a.s0, row_info(q, i).seq) : h);
           h = mul2(al[r], d);
           f2 dg = mul2(h, z);
           if (RAW) dg = mul2(dg, in[r]);
           store(static_cast<IO*>(a.out), elem(q, 0, i), i, COMPL ? mul2(in[r], d) : d, direct);
           store(static_cast<IO*>(a.dg), second(i), i, dg, direct);
         }
-        if (E && (kDown ? o.first : o.last) && a.sT) {
+        if (E && (stop >> r & 1) && a.sT) {
           float w[2];
           unpack(h, w[0], w[1]);
+          float* to = a.sT + (size_t)row_info(q, i).seq * a.D + q.c;
 #pragma unroll
           for (int j = 0; j < 2; ++j)
-            if (j < q.n) a.sT[(size_t)o.seq * a.D + q.c + j] = w[j];
+            if (j < q.n) to[j] = w[j];
         }
       }
     };
-    if (edge)
-      emit(std::true_type{});
-    else
-      emit(std::false_type{});
+    if (edge) {
+      emit(std::true_type{}, std::true_type{});
+    } else if (p.tma) {
+      emit(std::false_type{}, std::true_type{});
+    } else {
+      emit(std::false_type{}, std::false_type{});
+    }
 
     // ---- out by TMA, each unit's rows (rows past T are not written)
     if (p.tma) {
@@ -836,7 +843,6 @@ __global__ void __launch_bounds__(kThreads, Shape<K, IO, COMPL>::kPerSm)
         bulk_commit();
       }
     }
-    if (threadIdx.x == 0) advance();
   }
   if (lane == 0) bulk_wait_read();
   __syncwarp();
@@ -844,19 +850,31 @@ __global__ void __launch_bounds__(kThreads, Shape<K, IO, COMPL>::kPerSm)
   if (size > 1) asm volatile("barrier.cluster.arrive.release.aligned;\n barrier.cluster.wait.acquire.aligned;" ::: "memory");
 }
 
+// log(1 + e) for 0 <= e <= 1, as 2 artanh(s) with s = e / (2 + e) <= 1/3 (the series to s^13, 3e-8 off).
+__device__ __forceinline__ f2 log1p2_of(f2 e) {
+  float a, b;
+  unpack(add2(e, both(2.f)), a, b);
+  const f2 s = mul2(e, pack(rcp_of(a), rcp_of(b))), q = mul2(s, s);
+  f2 t = fma2(q, both(2.f / 13.f), both(2.f / 11.f));
+  t = fma2(q, t, both(2.f / 9.f));
+  t = fma2(q, t, both(2.f / 7.f));
+  t = fma2(q, t, both(2.f / 5.f));
+  t = fma2(q, t, both(2.f / 3.f));
+  t = fma2(q, t, both(2.f));
+  return mul2(s, t);
+}
+
 // The 8-bit checkpoint.  A block writes 128 channels (a row's scale block) of
 // four segments of the forward's rows; a thread holds two channels x one
 // segment, as there, and goes the same way from the state that entered the
-// segment's unit, so that z is what the forward saw.  8 B of traffic per
-// element in bf16 (x and g are read once more, from L2 for the rows that the
-// forward did last, which come first here); all loads of a thread are in
-// flight at once.
+// segment, so that z is what the forward saw.  8 B of traffic per element in
+// bf16 (x and g are read once more, from L2 for the rows that the forward did
+// last, which come first here); all loads of a thread are in flight at once.
 template <typename IO, bool RAW, bool COMPL>
 __global__ void __launch_bounds__(256, 2) scan_save_kernel(const __grid_constant__ TileArgs p) {
   using S = Shape<kFwd, IO, COMPL>;
   constexpr int R = S::kR, kSegs = 4;
-  __shared__ float2 pair[kSegs][kBlock];
-  __shared__ uint32_t top[8][2][R];
+  __shared__ uint32_t top[8][2][R];  // of a warp's rows, lambda and z: the largest magnitude
   __shared__ float inv[kSegs][2][R];
   const ScanArgs& a = p.a;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, across = threadIdx.x % 64, seg = threadIdx.x / 64;
@@ -871,20 +889,25 @@ __global__ void __launch_bounds__(256, 2) scan_save_kernel(const __grid_constant
   uint32_t x[R][kWords], g[R][kWords];
   const bool pairs = a.D % 2 == 0;
   const IO *px = static_cast<const IO*>(a.x) + row0 * a.D + c, *pg = static_cast<const IO*>(a.g) + row0 * a.D + c;
-  auto load = [&](const IO* q, bool in, uint32_t* to) {
-    if (pairs && in && n > 0) {
+  if (pairs && n > 0 && most == R) {
 #pragma unroll
-      for (int j = 0; j < kWords; ++j) to[j] = __ldg(reinterpret_cast<const uint32_t*>(q) + j);
-    } else {
+    for (int r = 0; r < R; ++r)
+#pragma unroll
+      for (int j = 0; j < kWords; ++j) {
+        x[r][j] = __ldg(reinterpret_cast<const uint32_t*>(px + (size_t)r * a.D) + j);
+        g[r][j] = __ldg(reinterpret_cast<const uint32_t*>(pg + (size_t)r * a.D) + j);
+      }
+  } else {
+    auto load = [&](const IO* q, bool in, uint32_t* to) {
       IO v[2] = {in && n > 0 ? q[0] : from_f32<IO>(0.f), in && n > 1 ? q[1] : from_f32<IO>(0.f)};
 #pragma unroll
       for (int j = 0; j < kWords; ++j) to[j] = reinterpret_cast<const uint32_t*>(v)[j];
-    }
-  };
+    };
 #pragma unroll
-  for (int r = 0; r < R; ++r) {
-    load(px + (size_t)r * a.D, r < most, x[r]);
-    load(pg + (size_t)r * a.D, r < most, g[r]);
+    for (int r = 0; r < R; ++r) {
+      load(px + (size_t)r * a.D, r < most, x[r]);
+      load(pg + (size_t)r * a.D, r < most, g[r]);
+    }
   }
   auto value = [](const uint32_t* w) {
     if constexpr (kWords == 1)
@@ -892,7 +915,7 @@ __global__ void __launch_bounds__(256, 2) scan_save_kernel(const __grid_constant
     else
       return pack(__uint_as_float(w[0]), __uint_as_float(w[1]));
   };
-  grid_dep_wait();  // what entered the units comes from the kernel before
+  grid_dep_wait();  // what entered the segments comes from the kernel before
   // bit r: whether row r belongs to a sequence, and whether it is one's first
   uint32_t valid = most > 0 ? (1u << most) - 1 : 0, first = t0 == 0 ? 1 : 0;
   if (a.cu) {
@@ -908,81 +931,95 @@ __global__ void __launch_bounds__(256, 2) scan_save_kernel(const __grid_constant
     ldg<2>(a.s0 ? a.s0 + (size_t)seq * a.D + c : nullptr, v, n, pairs);
     return pack(v[0], v[1]);
   };
-  float f[2] = {0.f, 0.f};
-  const int unit = part * (kSegs / S::kSide) + seg / S::kSide;
-  if (n > 0 && unit < p.chunks * kWarps) {
-    const size_t chain = (size_t)b * p.blocks + c / S::W;
-    const float2 e = *reinterpret_cast<const float2*>(p.enters + (chain * p.chunks * kWarps + unit) * S::W + c % S::W);
-    f[0] = e.x, f[1] = e.y;
+  f2 h = both(0.f), z[R], lam[R];
+  if (n > 0 && most > 0) {
+    const size_t chain = (size_t)b * p.blocks + c / S::W, segs = (size_t)p.chunks * kWarps * S::kSide;
+    const float2 e = *reinterpret_cast<const float2*>(p.enters + (chain * segs + part * kSegs + seg) * S::W + c % S::W);
+    h = pack(e.x, e.y);
   }
-  {
-    f2 A = both(1.f), B = both(0.f);
+  auto rows_of = [&](auto edges) {
+    constexpr bool E = decltype(edges)::value;
 #pragma unroll
     for (int r = 0; r < R; ++r) {
+      const f2 gv = value(g[r]);
       f2 al, be;
-      gate<RAW>(value(g[r]), al, be);
-      const f2 in = COMPL ? mul2(be, value(x[r])) : value(x[r]);
-      if (first >> r & 1) {
-        A = both(-0.f);
-        B = fma2(al, state_of(r), in);
-      } else if (valid >> r & 1) {
-        A = mul2(A, al);
-        B = fma2(al, B, in);
+      gate<RAW>(gv, al, be);
+      if (E && (first >> r & 1)) h = state_of(r);
+      z[r] = COMPL ? add2(h, neg2(value(x[r]))) : h;
+      const f2 u = COMPL ? mul2(be, value(x[r])) : value(x[r]);
+      if (!E || (valid >> r & 1)) h = fma2(al, h, u);
+      lam[r] = gv;
+      float f[2];
+      unpack(gv, f[0], f[1]);
+      if (RAW) {  // min(g, 0) - log(1 + exp(-|g|))
+        const f2 l = log1p2_of(exp2_of(pack(-min_nan(fabsf(f[0]), 128.f), -min_nan(fabsf(f[1]), 128.f))));
+        lam[r] = add2(pack(min_nan(f[0], 0.f), min_nan(f[1], 0.f)), neg2(l));
+      }
+      if (E) {
+        const bool in = valid >> r & 1;
+        unpack(lam[r], f[0], f[1]);
+        lam[r] = pack(in && n > 0 ? f[0] : 0.f, in && n > 1 ? f[1] : 0.f);
+        unpack(z[r], f[0], f[1]);
+        z[r] = pack(in && n > 0 ? f[0] : 0.f, in && n > 1 ? f[1] : 0.f);
       }
     }
-    float4 v;
-    unpack(A, v.x, v.z);
-    unpack(B, v.y, v.w);
-    *reinterpret_cast<float4*>(&pair[seg][across * 2]) = v;
-  }
-  __syncthreads();
-  for (int s = seg / S::kSide * S::kSide; s < seg; ++s)
+  };
+  if (first || valid != (1u << R) - 1 || n < 2)
+    rows_of(std::true_type{});
+  else
+    rows_of(std::false_type{});
+  // the largest magnitudes; non-finite values, which do not count, are looked for only where there are any
+  auto tops = [&](auto careful) {
 #pragma unroll
-    for (int j = 0; j < 2; ++j) f[j] = through(f[j], pair[s][across * 2 + j]);
-  f2 h = pack(f[0], f[1]), z[R];
+    for (int r = 0; r < R; ++r)
 #pragma unroll
-  for (int r = 0; r < R; ++r) {
-    f2 al, be;
-    gate<RAW>(value(g[r]), al, be);
-    if (first >> r & 1) h = state_of(r);
-    z[r] = both(0.f);
-    if (valid >> r & 1) {
-      z[r] = COMPL ? add2(h, neg2(value(x[r]))) : h;
-      h = fma2(al, h, COMPL ? mul2(be, value(x[r])) : value(x[r]));
+      for (int m = 0; m < 2; ++m) {
+        float f[2];
+        unpack(m ? z[r] : lam[r], f[0], f[1]);
+        const uint32_t u0 = decltype(careful)::value ? magnitude(f[0]) : __float_as_uint(f[0]) & 0x7fffffffu;
+        const uint32_t u1 = decltype(careful)::value ? magnitude(f[1]) : __float_as_uint(f[1]) & 0x7fffffffu;
+        const uint32_t t = __reduce_max_sync(0xffffffffu, max(u0, u1));
+        if (lane == 0) top[warp][m][r] = t;
+      }
+    __syncthreads();
+    bool odd = false;
+    if (across < 2 * R) {  // one scale each
+      const int m = across / R, r = across % R;
+      const uint32_t t = max(top[2 * seg][m][r], top[2 * seg + 1][m][r]);
+      odd = t >= 0x7f800000u;
+      const int code = scale_code(__uint_as_float(t));
+      inv[seg][m][r] = pow2(254 - code);
+      if (r < most && !odd) a.ckpt[(m ? lay.z_scale : lay.lam_scale) + cb * rows + row0 + r] = (uint8_t)code;
     }
-    unpack(z[r], f[0], f[1]);
-    const uint32_t m = __reduce_max_sync(0xffffffffu, max(magnitude(f[0]), magnitude(f[1])));
-    if (lane == 0) top[warp][1][r] = m;
-  }
-  f2 lam[R];
+    return __syncthreads_or(odd);
+  };
+  auto codes = [&](auto careful) {
+    if (n <= 0) return;
+    uint8_t* to = a.ckpt + row0 * lay.pitch + c;
 #pragma unroll
-  for (int r = 0; r < R; ++r) {
-    lam[r] = value(g[r]);
-    unpack(lam[r], f[0], f[1]);
-    const bool in = valid >> r & 1;
-    if (RAW) f[0] = log_sigmoid(f[0]), f[1] = log_sigmoid(f[1]);
-    f[0] = in && n > 0 ? f[0] : 0.f, f[1] = in && n > 1 ? f[1] : 0.f;
-    lam[r] = pack(f[0], f[1]);
-    const uint32_t m = __reduce_max_sync(0xffffffffu, max(magnitude(f[0]), magnitude(f[1])));
-    if (lane == 0) top[warp][0][r] = m;
-  }
-  __syncthreads();
-  if (across < 2 * R) {  // one scale each
-    const int m = across / R, r = across % R;
-    const int code = scale_code(__uint_as_float(max(top[2 * seg][m][r], top[2 * seg + 1][m][r])));
-    inv[seg][m][r] = pow2(254 - code);
-    if (r < most) a.ckpt[(m ? lay.z_scale : lay.lam_scale) + cb * rows + row0 + r] = (uint8_t)code;
-  }
-  __syncthreads();
-  if (n <= 0) return;
-  uint8_t* to = a.ckpt + row0 * lay.pitch + c;
+    for (int r = 0; r < R; ++r, to += lay.pitch) {
+      if (r >= most) break;
 #pragma unroll
-  for (int r = 0; r < R; ++r, to += lay.pitch) {
-    if (r >= most) break;
-    unpack(lam[r], f[0], f[1]);
-    *reinterpret_cast<uint16_t*>(to) = encode2(f, inv[seg][0][r]);
-    unpack(z[r], f[0], f[1]);
-    *reinterpret_cast<uint16_t*>(to + lay.z) = encode2(f, inv[seg][1][r]);
+      for (int m = 0; m < 2; ++m) {
+        float f[2];
+        const float by = inv[seg][m][r];
+        if (decltype(careful)::value) {
+          unpack(m ? z[r] : lam[r], f[0], f[1]);
+          f[0] = finite(f[0]) ? f[0] * by : __int_as_float(0x7fffffff);
+          f[1] = finite(f[1]) ? f[1] * by : __int_as_float(0x7fffffff);
+        } else {
+          unpack(mul2(m ? z[r] : lam[r], both(by)), f[0], f[1]);
+        }
+        *reinterpret_cast<uint16_t*>(to + (m ? lay.z : 0)) =
+            __nv_cvt_float2_to_fp8x2(make_float2(f[0], f[1]), __NV_SATFINITE, __NV_E4M3);
+      }
+    }
+  };
+  if (tops(std::false_type{})) {
+    tops(std::true_type{});
+    codes(std::true_type{});
+  } else {
+    codes(std::false_type{});
   }
 }
 
@@ -1158,7 +1195,7 @@ cudaError_t launch_tiles(const ScanArgs& a, void* ws, cudaStream_t stream) {
   p.tma = (size_t)a.D * sizeof(IO) % 16 == 0;
   p.words = (size_t)a.D * sizeof(IO) % 4 == 0;
   uint8_t* w = static_cast<uint8_t*>(ws);
-  p.hdr = reinterpret_cast<WorkspaceHeader*>(w);
+  p.hdr = ws ? reinterpret_cast<WorkspaceHeader*>(w) : nullptr;
   w += sizeof(WorkspaceHeader);
   p.pairs = reinterpret_cast<float*>(w);
   p.states = p.pairs + plan.pair_words;
@@ -1172,10 +1209,10 @@ cudaError_t launch_tiles(const ScanArgs& a, void* ws, cudaStream_t stream) {
   const ScanCkptLayout l = scan_ckpt_layout((size_t)a.B * a.T, a.D);
   bool ok = true;
   for (int i = 0; i < S::kIn; ++i) {
-    if (K == kBwdCkpt && i > 0)
-      ok = ok && make_map(&p.map[i], a.ckpt + (i == 2 ? l.z : 0), 1, a.B, a.T, a.D, l.pitch, S::W, S::kBox);
+    if (S::kFrom && i > 0)
+      ok = ok && make_map(&p.map[i], a.ckpt + (i == 2 ? l.z : 0), 1, a.B, a.T, a.D, l.pitch, S::W, S::kL);
     else if (p.tma)
-      ok = ok && make_map(&p.map[i], arrays[i], sizeof(IO), a.B, a.T, a.D, a.D, S::W, S::kBox);
+      ok = ok && make_map(&p.map[i], arrays[i], sizeof(IO), a.B, a.T, a.D, a.D, S::W, S::kL);
   }
   if (p.tma) ok = ok && make_map(&p.out[0], a.out, sizeof(IO), a.B, a.T, a.D, a.D, S::W, S::kUnitRows);
   if (p.tma && S::kDown) ok = ok && make_map(&p.out[1], a.dg, sizeof(IO), a.B, a.T, a.D, a.D, S::W, S::kUnitRows);
@@ -1214,23 +1251,24 @@ cudaError_t launch_tiles(const ScanArgs& a, void* ws, cudaStream_t stream) {
 // Enough for every kind of call of these sizes: the header, the words handed
 // between blocks, the rows' information if packed, the forward's states at its
 // units for the checkpoint.
-size_t scan_workspace_bytes(int B, int T, int D, int N, int dtype) {
+size_t scan_workspace_bytes(int B, int T, int D, int N, int dtype, bool checkpoint) {
   if (B == 0 || T == 0) return 0;
   size_t words = 0, enters = 0;
   const auto fit = [&](const Plan& q) { words = std::max(words, q.pair_words + q.state_words); };
   const auto fit_all = [&](auto io) {
     using IO = decltype(io);
     const Plan f = plan_for<kFwd, IO, false>(B, T, D);
-    enters = (size_t)(f.chains * f.chunks) * kWarps * Shape<kFwd, IO, false>::W;
+    enters = (size_t)(f.chains * f.chunks) * kWarps * Shape<kFwd, IO, false>::kSide * Shape<kFwd, IO, false>::W;
     fit(f), fit(plan_for<kFwd, IO, true>(B, T, D));
     fit(plan_for<kBwd, IO, false>(B, T, D)), fit(plan_for<kBwd, IO, true>(B, T, D));
-    fit(plan_for<kBwdCkpt, IO, false>(B, T, D));
+    fit(plan_for<kBwdCkpt, IO, false>(B, T, D)), fit(plan_for<kBwdCkptNarrow, IO, false>(B, T, D));
   };
   if (dtype == KDA_F32)
     fit_all(float{});
   else
     fit_all(__nv_bfloat16{});
-  return sizeof(WorkspaceHeader) + align256(words * 4) + (N > 0 ? info_bytes(T) : 0) + align256(enters * 4);
+  const size_t bytes = align256(words * 4) + (N > 0 ? info_bytes(T) : 0) + (checkpoint ? align256(enters * 4) : 0);
+  return bytes ? sizeof(WorkspaceHeader) + bytes : 0;
 }
 
 cudaError_t launch_scan_fwd(const ScanArgs& a, void* ws, cudaStream_t stream) {
@@ -1241,8 +1279,12 @@ cudaError_t launch_scan_fwd(const ScanArgs& a, void* ws, cudaStream_t stream) {
 
 cudaError_t launch_scan_bwd(const ScanArgs& a, void* ws, cudaStream_t stream) {
   return with_flags(a.dtype, a.prep, a.complement, [&](auto io, auto raw, auto compl_) {
-    return a.ckpt ? launch_tiles<kBwdCkpt, decltype(io), raw.value, compl_.value>(a, ws, stream)
-                  : launch_tiles<kBwd, decltype(io), raw.value, compl_.value>(a, ws, stream);
+    using IO = decltype(io);
+    if (!a.ckpt) return launch_tiles<kBwd, IO, raw.value, compl_.value>(a, ws, stream);
+    if constexpr (sizeof(IO) == 2)
+      if ((int64_t)a.B * div_up(a.D, 64) >= kWideChains)
+        return launch_tiles<kBwdCkpt, IO, raw.value, compl_.value>(a, ws, stream);
+    return launch_tiles<kBwdCkptNarrow, IO, raw.value, compl_.value>(a, ws, stream);
   });
 }
 

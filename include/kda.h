@@ -371,11 +371,18 @@ KDA_API kda_status kda_recurrent_step_ex(const void* q, const void* k, const voi
 typedef enum { KDA_SCAN_INPUT_PLAIN = 0, KDA_SCAN_INPUT_COMPLEMENT = 1 } kda_scan_input;
 
 /*
- * Bytes of device workspace kda_scan_fwd, kda_scan_backward and
- * kda_scan_backward_ckpt need (0 if none, and for arguments they reject).
+ * Bytes of device workspace that kda_scan_fwd without a checkpoint,
+ * kda_scan_backward and kda_scan_backward_ckpt need; 0 if none (for many sizes;
+ * NULL is then allowed), and for arguments they reject.
  * `num_seqs`: the number of packed sequences, 0 without cu_seqlens.
  */
 KDA_API size_t kda_scan_workspace_size(int B, int T, int D, int num_seqs, int dtype);
+
+/*
+ * The same, and with `checkpoint` nonzero what a kda_scan_fwd that writes the
+ * checkpoint needs, which is never less.
+ */
+KDA_API size_t kda_scan_workspace_size_ex(int B, int T, int D, int num_seqs, int dtype, int checkpoint);
 
 /*
  * Bytes of the 8-bit activation checkpoint of B x T rows of D channels (0 for
@@ -404,7 +411,7 @@ KDA_API size_t kda_scan_checkpoint_size(int B, int T, int D);
  *                   checkpoint is written
  *   checkpoint    : NULL, or kda_scan_checkpoint_size() bytes, 16-byte
  *                   aligned, written beside h
- *   workspace     : kda_scan_workspace_size() bytes, 256-byte aligned,
+ *   workspace     : kda_scan_workspace_size_ex() bytes, 256-byte aligned,
  *                   contents on entry do not matter; not shared by two calls
  *                   in flight (two captured graphs among them).  Its header is
  *                   read by kda_chunk_fwd_check: KDA_ERR_TIMEOUT if a bounded

@@ -95,6 +95,18 @@ def test_workspace(lib):
     assert c(1, 1, 1) == 1024
 
 
+@pytest.mark.parametrize("kw,size", [(dict(ckpt=at(12)), (2, 300, 256, 0, 1, 1)),
+                                     (dict(B=1, cu=at(10), n=3), (1, 300, 256, 3, 1, 0)),
+                                     (dict(B=1, T=100000, D=64), (1, 100000, 64, 0, 1, 0))],
+                         ids=["checkpoint", "packed", "few-chains"])
+def test_workspace_is_asked_for(lib, kw, size):
+    need = lib.kda_scan_workspace_size_ex(*size)
+    assert need > 0 and lib.kda_scan_workspace_size_ex(*size[:5], 1) >= need
+    for bad in (dict(ws=None), dict(wsb=need - 1), dict(ws=at(8) + 16), dict(ws=at(3)), dict(ws=at(1))):
+        assert fwd(lib, **kw, **bad) == BAD, bad
+    assert lib.kda_scan_workspace_size(*size[:5]) == lib.kda_scan_workspace_size_ex(*size[:5], 0)
+
+
 def test_step(lib):
     def step(x=at(0), g=at(1), s=at(2), o=at(2), h=at(3), N=4, D=256, dtype=1, prep=0, ig=0):
         return lib.kda_scan_step(x, g, s, o, h, N, D, dtype, prep, ig, None)
