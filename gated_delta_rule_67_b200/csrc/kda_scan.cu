@@ -136,21 +136,24 @@ __device__ __forceinline__ f2 exp2_of(f2 x) {
   const f2 e = pack(ex2_of(a), ex2_of(b));
   return fma2(e, fma2(p, both(-0.693147181f), x), e);
 }
-// alpha and 1 - alpha of two gates, each to a few ulp on its own.  The clamps
-// keep the exponent's residual a number; past them exp is below 2^-126 and
-// counts as zero.  NaN stays NaN.  For a given log-gate, 1 - alpha is the
-// series where the difference would lose the small rates that make the long
-// memories.
-template <bool RAW>
+// alpha and, with RATE, 1 - alpha of two gates, each to a few ulp on its own:
+// the small rates make the long memories, and a difference would lose them.
+// Near 1, where its rounding counts for as many rows as the memory is long,
+// alpha is rounded once: the reciprocal gets a Newton step, and a given
+// log-gate's exp is 1 + its series.  The clamps keep the exponent's residual a
+// number; past them exp is below 2^-126 and counts as zero.  NaN stays NaN.
+template <bool RAW, bool RATE>
 __device__ __forceinline__ void gate(f2 g, f2& alpha, f2& beta) {
   float g0, g1;
   unpack(g, g0, g1);
   if (RAW) {
-    const f2 e = exp2_of(pack(-min_nan(fabsf(g0), 128.f), -min_nan(fabsf(g1), 128.f)));
+    const f2 e = exp2_of(pack(-min_nan(fabsf(g0), 128.f), -min_nan(fabsf(g1), 128.f))), s = add2(e, both(1.f));
     float s0, s1, l0, l1;
-    unpack(add2(e, both(1.f)), s0, s1);
-    s0 = rcp_of(s0), s1 = rcp_of(s1);
-    unpack(mul2(e, pack(s0, s1)), l0, l1);
+    unpack(s, s0, s1);
+    f2 hi = pack(rcp_of(s0), rcp_of(s1));
+    hi = fma2(hi, fma2(neg2(s), hi, both(1.f)), hi);
+    unpack(hi, s0, s1);
+    unpack(mul2(e, hi), l0, l1);
     const bool p0 = g0 >= 0.f, p1 = g1 >= 0.f;
     alpha = pack(p0 ? s0 : l0, p1 ? s1 : l1);
     beta = pack(p0 ? l0 : s0, p1 ? l1 : s1);
@@ -158,6 +161,7 @@ __device__ __forceinline__ void gate(f2 g, f2& alpha, f2& beta) {
     const float x0 = max_nan(g0, -128.f), x1 = max_nan(g1, -128.f);
     const f2 x = pack(x0, x1);
     alpha = exp2_of(x);
+    if (!RATE) return;
     f2 q = fma2(x, both(1.f / 40320.f), both(1.f / 5040.f));
     q = fma2(x, q, both(1.f / 720.f));
     q = fma2(x, q, both(1.f / 120.f));
@@ -165,10 +169,13 @@ __device__ __forceinline__ void gate(f2 g, f2& alpha, f2& beta) {
     q = fma2(x, q, both(1.f / 6.f));
     q = fma2(x, q, both(0.5f));
     q = fma2(x, q, both(1.f));
-    float a0, a1, q0, q1;
+    float a0, a1, n0, n1, q0, q1;
     unpack(alpha, a0, a1);
+    unpack(fma2(x, q, both(1.f)), n0, n1);
     unpack(mul2(x, q), q0, q1);
-    beta = pack(fabsf(x0) < 0.5f ? -q0 : 1.f - a0, fabsf(x1) < 0.5f ? -q1 : 1.f - a1);
+    const bool p0 = fabsf(x0) < 0.5f, p1 = fabsf(x1) < 0.5f;
+    alpha = pack(p0 ? n0 : a0, p1 ? n1 : a1);
+    beta = pack(p0 ? -q0 : 1.f - a0, p1 ? -q1 : 1.f - a1);
   }
 }
 
@@ -635,12 +642,12 @@ __global__ void __launch_bounds__(kThreads, Shape<K, IO, COMPL>::kPerSm)
 #pragma unroll
       for (int r = 0; r < R; ++r) {
         const int i = row_at(r);
-        f2 g, be;
+        f2 g, be = 0;
         if constexpr (kFrom) g = codes_of(q, 1, i);
         else g = load2(q, 1, i);
         const f2 x = load2(q, 0, i);
-        gate<RAW && !kFrom>(g, al[r], be);
-        in[r] = kDown ? be : COMPL ? mul2(be, x) : x;
+        gate<RAW && !kFrom, RAW || COMPL>(g, al[r], be);
+        in[r] = kDown && (RAW || COMPL) ? be : COMPL ? mul2(be, x) : x;
         if (E && !(valid >> r & 1)) continue;
         if (E && (start >> r & 1)) {
           const f2 f = state_of(q, a.s0, row_info(q, i).seq);
@@ -942,8 +949,8 @@ __global__ void __launch_bounds__(256, 2) scan_save_kernel(const __grid_constant
 #pragma unroll
     for (int r = 0; r < R; ++r) {
       const f2 gv = value(g[r]);
-      f2 al, be;
-      gate<RAW>(gv, al, be);
+      f2 al, be = 0;
+      gate<RAW, COMPL>(gv, al, be);
       if (E && (first >> r & 1)) h = state_of(r);
       z[r] = COMPL ? add2(h, neg2(value(x[r]))) : h;
       const f2 u = COMPL ? mul2(be, value(x[r])) : value(x[r]);
@@ -1079,8 +1086,8 @@ __global__ void __launch_bounds__(256) scan_step_kernel(const IO* __restrict__ x
   ldg<4>(state + i, s, n, n == 4);
 #pragma unroll
   for (int j = 0; j < 4; j += 2) {
-    f2 alpha, beta;
-    gate<RAW>(pack(gv[j], gv[j + 1]), alpha, beta);
+    f2 alpha, beta = 0;
+    gate<RAW, COMPL>(pack(gv[j], gv[j + 1]), alpha, beta);
     const f2 v = pack(xv[j], xv[j + 1]);
     unpack(fma2(alpha, pack(s[j], s[j + 1]), COMPL ? mul2(beta, v) : v), s[j], s[j + 1]);
   }
