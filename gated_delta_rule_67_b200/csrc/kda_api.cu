@@ -325,7 +325,7 @@ kda_status kda_recurrent_step_ex(const void* q, const void* k, const void* v, co
 static kda_status scan_sizes(int64_t B, int64_t T, int64_t D, int64_t N, int dtype) {
   if (B < 0 || T < 0 || D < 1 || N < 0) return KDA_ERR_INVALID_ARG;
   if (dtype != KDA_F32 && dtype != KDA_BF16) return KDA_ERR_INVALID_ARG;
-  if (T > INT32_MAX - 1024) return KDA_ERR_UNSUPPORTED;  // row numbers of a last tile stay within 32 bits
+  if (T > INT32_MAX - 4096) return KDA_ERR_UNSUPPORTED;  // row numbers of a last tile stay within 32 bits
   constexpr int64_t kMost = (int64_t)1 << 40;
   if (B * D > kMost || N * D > kMost || (T > 0 && B * D > kMost / T)) return KDA_ERR_UNSUPPORTED;
   if (B * ((D + 15) / 16) * ((T + 63) / 64) > INT32_MAX || N > (1 << 28)) return KDA_ERR_UNSUPPORTED;

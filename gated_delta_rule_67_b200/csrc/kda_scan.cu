@@ -41,7 +41,7 @@
 //
 // The 8-bit checkpoint needs the largest magnitude of a row's 128 channels,
 // several chains: a second kernel writes it, each block for itself, from the
-// states that the first leaves at every unit of rows.
+// states that the first leaves at every segment.
 #include <cudaTypedefs.h>
 #include <cuda_fp8.h>
 
@@ -61,23 +61,27 @@ constexpr int kWarps = 8;
 constexpr int kThreads = 32 * kWarps;
 constexpr int kGroup = 16;      // few chains: tiles from one published state to the next
 constexpr int kCluster = 8;     // blocks that walk a chain together, at most
-constexpr int kJoinChains = 16; // fewer chains, of more than
-constexpr int kWideChains = 128;  // chains of 64 channels from which the backward from the checkpoint takes them
-constexpr int kJoinTiles = 32;  // so many tiles each, are joined tile by tile
+// Fewer chains than this, of more tiles than this each, are joined tile by tile instead of walked (bf16 forward,
+// 65536 rows: 2 chains 44 us against 88, 8 chains 73 against 90; 15 chains 100 against 91, 32 chains 171 against 107).
+constexpr int kJoinChains = 12, kJoinTiles = 32;
+// Chains of 64 channels from which on the backward from the checkpoint takes them (see Shape).
+constexpr int kWideChains = 128;
 constexpr int kInfoPad = 512;   // rows of padding behind the packed sequences' row information
 constexpr uint32_t kEmpty = 0xffffffffu;     // a word not yet written
-constexpr uint64_t kGiveUp = 2000000000;     // ns after which a wait gives up
+// A wait gives up after both: ns, and looks (a program that was set aside meanwhile gets its looks afterwards).
+constexpr uint64_t kGiveUp = 2000000000;
+constexpr uint32_t kLooks = 1u << 20;
 
 __device__ __forceinline__ uint64_t now_ns() {
   uint64_t t;
   asm volatile("mov.u64 %0, %%globaltimer;" : "=l"(t));
   return t;
 }
-// Waits for a phase of `bar`; false after kGiveUp.
+// Waits for a phase of `bar`; false if it gave up.
 __device__ __forceinline__ bool wait_for(uint64_t* bar, uint32_t parity) {
   if (mbar_try_wait(bar, parity)) return true;
   const uint64_t since = now_ns();
-  while (now_ns() - since < kGiveUp)
+  for (uint32_t i = 0; i < kLooks || now_ns() - since < kGiveUp; ++i)
     if (mbar_try_wait(bar, parity)) return true;
   return false;
 }
@@ -605,8 +609,8 @@ __global__ void __launch_bounds__(kThreads, Shape<K, IO, COMPL>::kPerSm)
     auto arrived = [&](const float* at, uint32_t v) {
       if (v == kEmpty && !failed) {
         const uint64_t since = now_ns();
-        while ((v = peek(at)) == kEmpty)
-          if (now_ns() - since > kGiveUp) {
+        for (uint32_t i = 0; (v = peek(at)) == kEmpty; ++i)
+          if (i >= kLooks && now_ns() - since > kGiveUp) {
             failed = true;
             gave_up(203);
             break;
@@ -697,7 +701,7 @@ __global__ void __launch_bounds__(kThreads, Shape<K, IO, COMPL>::kPerSm)
           for (int w = 1; w < kWarps; ++w) t[j] = joined(t[j], pair[w][ch + j]);
         }
       }
-      if (!wait_for(&sh.came[k & 1], (k >> 1) & 1)) gave_up(204);
+      if (!failed && !wait_for(&sh.came[k & 1], (k >> 1) & 1)) failed = true, gave_up(204);
 #pragma unroll
       for (int j = 0; j < kCh; ++j) e[j] = q.chunk > 0 ? sh.inbox[k & 1][ch + j] : 0.f;
       if (warp == 0 && q.chunk + 1 < p.chunks) {  // on to the block that has the next tile
@@ -857,6 +861,8 @@ __global__ void __launch_bounds__(kThreads, Shape<K, IO, COMPL>::kPerSm)
   if (size > 1) asm volatile("barrier.cluster.arrive.release.aligned;\n barrier.cluster.wait.acquire.aligned;" ::: "memory");
 }
 
+constexpr float kLeast = -128.f;  // lambda in the checkpoint: exp is zero in fp32 from there on
+
 // log(1 + e) for 0 <= e <= 1, as 2 artanh(s) with s = e / (2 + e) <= 1/3 (the series to s^13, 3e-8 off).
 __device__ __forceinline__ f2 log1p2_of(f2 e) {
   float a, b;
@@ -955,12 +961,12 @@ __global__ void __launch_bounds__(256, 2) scan_save_kernel(const __grid_constant
       z[r] = COMPL ? add2(h, neg2(value(x[r]))) : h;
       const f2 u = COMPL ? mul2(be, value(x[r])) : value(x[r]);
       if (!E || (valid >> r & 1)) h = fma2(al, h, u);
-      lam[r] = gv;
       float f[2];
       unpack(gv, f[0], f[1]);
+      lam[r] = pack(max_nan(f[0], kLeast), max_nan(f[1], kLeast));
       if (RAW) {  // min(g, 0) - log(1 + exp(-|g|))
         const f2 l = log1p2_of(exp2_of(pack(-min_nan(fabsf(f[0]), 128.f), -min_nan(fabsf(f[1]), 128.f))));
-        lam[r] = add2(pack(min_nan(f[0], 0.f), min_nan(f[1], 0.f)), neg2(l));
+        lam[r] = add2(pack(max_nan(min_nan(f[0], 0.f), kLeast), max_nan(min_nan(f[1], 0.f), kLeast)), neg2(l));
       }
       if (E) {
         const bool in = valid >> r & 1;
@@ -1257,7 +1263,7 @@ cudaError_t launch_tiles(const ScanArgs& a, void* ws, cudaStream_t stream) {
 
 // Enough for every kind of call of these sizes: the header, the words handed
 // between blocks, the rows' information if packed, the forward's states at its
-// units for the checkpoint.
+// segments for the checkpoint.
 size_t scan_workspace_bytes(int B, int T, int D, int N, int dtype, bool checkpoint) {
   if (B == 0 || T == 0) return 0;
   size_t words = 0, enters = 0;

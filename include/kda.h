@@ -389,7 +389,8 @@ KDA_API size_t kda_scan_workspace_size_ex(int B, int T, int D, int num_seqs, int
  * bad sizes): two bytes and a little per element, against four (fp32: eight)
  * for the activations it stands for, six (twelve) with KDA_SCAN_INPUT_COMPLEMENT.
  *
- * It holds all that the backward multiplies: lambda_t, and
+ * It holds all that the backward multiplies: lambda_t (no less than -128,
+ * where exp is zero in fp32, so a gate of minus infinity keeps its meaning), and
  * z_t = h_{t-1} (PLAIN) or h_{t-1} - x_t (COMPLEMENT), the factor of
  * d alpha_t; z of a sequence's first row contains its initial state.  Each is
  * e4m3 with one power-of-two scale 2^k per row and block of 128 channels

@@ -128,6 +128,9 @@ def scan_abs(alpha, u, first, reverse=False):
 
 
 # ----------------------------------------------------------------- checkpoint
+LEAST = -128.0  # lambda is held no lower: exp of it is zero in fp32
+
+
 def layout(rows, D):
     """(P, K, byte offsets of lambda codes, z codes, lambda scales, z scales, and the size)."""
     up = lambda v: -(-v // 256) * 256

@@ -296,6 +296,25 @@ def test_checkpoint_extremes():
     np.testing.assert_array_equal(z, want)
 
 
+@pytest.mark.parametrize("raw", [False, True])
+def test_checkpoint_of_gates_that_forget_everything(raw):
+    """Gates of minus infinity, of the types' lowest values and below -128 are held as -128: rows before them
+    get no gradient through them, and nothing turns into NaN."""
+    dev = cuda_or_skip()
+    T, D = 150, 136
+    x, g, s0, dh, dsT = make(1, T, D, torch.bfloat16, raw, 95)
+    lowest = torch.finfo(torch.bfloat16).min
+    g[0, 40], g[0, 80, ::2], g[0, 81, 1::2], g[0, 120, :5] = -float("inf"), lowest, -3e4, -200.0
+    ckpt = torch.empty(kda_scan_checkpoint_size(1, T, D), dtype=torch.uint8, device=dev)
+    kda_scan_fwd(x.to(dev), g.to(dev), s0.to(dev), checkpoint=ckpt, **how(raw, False))
+    lam8, z8, _, _ = scan.unpack(ckpt.cpu().numpy(), 1, T, D)
+    lam = np.maximum(scan.log_gate(g, raw), scan.LEAST)
+    assert np.all(np.abs(lam8 - lam) <= np.maximum(np.abs(lam) * 2.0 ** -4, 2.0 ** -11) * 1.01)
+    assert np.all(lam8[0, 40] == scan.LEAST)
+    got = kda_scan_backward_ckpt(ckpt, dh.to(dev), dsT.to(dev), **how(raw, False))
+    check_backward(got, lam8, z8, dh, dsT, raw, False)
+
+
 def test_checkpoint_bytes_are_scale_times_code():
     """Values that e4m3 holds come back unchanged, on every power of two."""
     dev = cuda_or_skip()
