@@ -467,10 +467,10 @@ def _train(x, g, s0, dh, dsT, kw, ckpt, **ws):
     return [h, sT] + [d[n] for d in (a, b) for n in ("dx", "dg", "dS0")]
 
 
-SAME = [(2, 700, 136, None), (1, 3000, 264, None), (1, 1500, 130, [3, 70, 70, 900, 1499])]
+SAME = [(2, 700, 136, None), (1, 3000, 264, None), (1, 1500, 130, [3, 70, 70, 900, 1499]), (1, 9000, 96, None)]
 
 
-@pytest.mark.parametrize("B,T,D,cu", SAME, ids=["two", "one", "packed"])
+@pytest.mark.parametrize("B,T,D,cu", SAME, ids=["two", "one", "packed", "few-chains"])
 def test_same_bits_every_time(B, T, D, cu):
     dev = cuda_or_skip()
     v = [t.to(dev) for t in make(B, T, D, torch.bfloat16, True, 150, cu)]
@@ -481,7 +481,7 @@ def test_same_bits_every_time(B, T, D, cu):
             assert torch.equal(a, b)
 
 
-@pytest.mark.parametrize("B,T,D,cu", SAME, ids=["two", "one", "packed"])
+@pytest.mark.parametrize("B,T,D,cu", SAME, ids=["two", "one", "packed", "few-chains"])
 def test_graph_replay_matches_eager(B, T, D, cu):
     """Captured once, replayed on new inputs (and new sequence boundaries), with an eager call of the same
     kind between the replays; a dirty workspace."""
@@ -513,11 +513,12 @@ def test_graph_replay_matches_eager(B, T, D, cu):
     assert size == 0 or kda_chunk_fwd_check(ws) == KDA_OK
 
 
-def test_two_streams_at_once():
+@pytest.mark.parametrize("T,D", [(5000, 512), (20000, 96), (3000, 4096)], ids=["walked", "joined", "many"])
+def test_two_streams_at_once(T, D):
     """Two calls in flight on two streams, each with its own workspace; and the ``stream`` argument."""
     dev = cuda_or_skip()
     kw = how(True, False)
-    v = [[t.to(dev) for t in make(1, 5000, 512, torch.bfloat16, True, s)] for s in (170, 171)]
+    v = [[t.to(dev) for t in make(1, T, D, torch.bfloat16, True, s)] for s in (170, 171)]
     ref = [kda_scan_fwd(a[0], a[1], a[2], **kw) for a in v]
     torch.cuda.synchronize()
     streams = [torch.cuda.Stream(dev) for _ in range(2)]
@@ -526,6 +527,40 @@ def test_two_streams_at_once():
         torch.cuda.synchronize()
         for p, q in zip(got, ref):
             assert torch.equal(p[0], q[0]) and torch.equal(p[1], q[1])
+
+
+@pytest.mark.parametrize("B,T,D,cu", [(1, 4000, 136, None), (3, 900, 2048, None), (1, 9000, 40, None),
+                                      (1, 5000, 1000, [0, 30, 30, 2000, 2001, 4999])],
+                         ids=["walked", "many", "joined", "packed"])
+def test_state_in_place_over_many_tiles(B, T, D, cu):
+    """final_state in initial_state's buffer gives the bits of two buffers."""
+    dev = cuda_or_skip()
+    x, g, s0, _, _ = (t.to(dev) for t in make(B, T, D, torch.bfloat16, True, 185, cu))
+    for _ in range(3):
+        h, sT = kda_scan_fwd(x, g, s0, **how(True, True, cu))
+        state = s0.clone()
+        h2, s2 = kda_scan_fwd(x, g, state, final_state=state, **how(True, True, cu))
+        assert s2 is state and torch.equal(h, h2) and torch.equal(sT, state)
+
+
+@pytest.mark.parametrize("cu", [[5, 3, 9, 200, 100, 150], [-7, 10, 400], [300, 200, 100], [2 ** 31 - 1, 0, -2 ** 31, 64]])
+def test_meaningless_boundaries_stay_in_bounds(cu):
+    """cu_seqlens that is not non-decreasing within [0, T]: whatever comes out, nothing outside the buffers is
+    touched (the sentinels around them), and the next call is right."""
+    dev = cuda_or_skip()
+    T, D = 150, 72
+    x, g, s0, dh, dsT = (t.to(dev) for t in make(1, T, D, torch.bfloat16, False, 190, cu))
+    n, N = T * D, len(cu) - 1
+    big = torch.full((n + 512,), 7.0, dtype=torch.bfloat16, device=dev)
+    sbig = torch.full((N * D + 128,), 5.0, device=dev)
+    kw = how(False, False, cu)
+    kda_scan_fwd(x, g, s0, h=big[256:256 + n].view(1, T, D), final_state=sbig[64:64 + N * D].view(N, D), **kw)
+    kda_scan_backward(None, g, x, dh, s0, dsT, **kw)
+    torch.cuda.synchronize()
+    assert (big[:256] == 7).all() and (big[256 + n:] == 7).all()
+    assert (sbig[:64] == 5).all() and (sbig[64 + N * D:] == 5).all()
+    x, g, s0, _, _ = make(1, 100, 40, torch.float32, False, 191)
+    check_forward(x, g, s0, False, False)
 
 
 def test_buffers_beside_the_outputs_stay():
