@@ -9,6 +9,7 @@ the compiled library or a CUDA device every call raises.
 from __future__ import annotations
 
 import ctypes
+import functools
 import os
 
 import torch
@@ -365,7 +366,7 @@ def kda_scan_checkpoint_size(B, T, D) -> int:
 # The scan calls are short on the device, so their checks are kept short here: one test of everything, and
 # only where it fails the one that names the fault.
 def _same(name, x, shape, dtype, device):
-    if not (isinstance(x, torch.Tensor) and x.dtype == dtype and x.device == device and x.shape == shape
+    if not (isinstance(x, torch.Tensor) and x.dtype is dtype and x.shape == shape and x.device == device
             and x.is_contiguous()):
         _check_dev(name, x, dtype)
         raise ValueError(f"{name} must be {list(shape)} on {device}, not {list(x.shape)} on {x.device}")
@@ -390,10 +391,21 @@ def _at(x):
     return None if x is None else x.data_ptr()
 
 
+# The workspace of a scan call depends on these sizes alone.
+@functools.lru_cache(maxsize=1024)
+def _scan_need(B, T, D, seqs, code, checkpoint):
+    return int(load().kda_scan_workspace_size_ex(B, T, D, seqs, code, checkpoint))
+
+
+def _state_like(given, shape, device):
+    """An fp32 state of `shape`; a state of that shape at hand makes it quicker."""
+    return torch.empty(shape, dtype=torch.float32, device=device) if given is None else torch.empty_like(given)
+
+
 def _scan_call(name, device, stream, args, made):
     """One call of the library on the device's stream.  ``made``: the tensors allocated here, which a stream
     other than the current one must be recorded with."""
-    fn = getattr(load(), name)
+    fn = getattr(_lib or load(), name)
     index = device.index
     current = torch._C._cuda_getCurrentRawStream(index)
     raw = current if stream is None else stream.cuda_stream
@@ -412,7 +424,7 @@ def _scan_call(name, device, stream, args, made):
 def _scan_workspace(workspace, x, B, T, D, seqs, code, checkpoint, made):
     """(address, bytes) of the caller's workspace or of one made here."""
     if workspace is None:
-        need = load().kda_scan_workspace_size_ex(B, T, D, seqs, code, checkpoint)
+        need = _scan_need(B, T, D, seqs, code, checkpoint)
         if not need:
             return None, 0
         workspace = torch.empty(need, dtype=torch.uint8, device=x.device)
@@ -453,7 +465,7 @@ def kda_scan_fwd(x, g, initial_state=None, *, cu_seqlens=None, input_gate=KDA_SC
     if final_state is not None:
         _same("final_state", final_state, state, torch.float32, device)
     elif output_final_state:
-        final_state = torch.empty(state, dtype=torch.float32, device=device)
+        final_state = _state_like(initial_state, state, device)
         made.append(final_state)
     if checkpoint is not None:
         _check_ckpt(checkpoint, x.shape, device)
@@ -471,10 +483,10 @@ def _check_ckpt(checkpoint, shape, device):
         raise ValueError(f"checkpoint must hold {need} bytes on {device}")
 
 
-def _scan_grads(like, state, want_initial_state_grad, made):
+def _scan_grads(like, state, given, want_initial_state_grad, made):
     out = dict(dx=torch.empty_like(like), dg=torch.empty_like(like), dS0=None)
     if want_initial_state_grad:
-        out["dS0"] = torch.empty(state, dtype=torch.float32, device=like.device)
+        out["dS0"] = _state_like(given, state, like.device)
     made.extend(t for t in out.values() if t is not None)
     return out
 
@@ -501,7 +513,8 @@ def kda_scan_backward(x, g, h, grad_h, initial_state=None, grad_final_state=None
     if grad_final_state is not None:
         _same("grad_final_state", grad_final_state, state, torch.float32, device)
     made = []
-    out = _scan_grads(grad_h, state, want_initial_state_grad, made)
+    out = _scan_grads(grad_h, state, grad_final_state if grad_final_state is not None else initial_state,
+                      want_initial_state_grad, made)
     ws, nbytes = _scan_workspace(workspace, grad_h, B, T, D, seqs, code, 0, made)
     _scan_call("kda_scan_backward", device, stream,
                (_at(x), g.data_ptr(), h.data_ptr(), _at(initial_state), grad_h.data_ptr(), _at(grad_final_state),
@@ -523,7 +536,7 @@ def kda_scan_backward_ckpt(checkpoint, grad_h, grad_final_state=None, *, cu_seql
         _same("grad_final_state", grad_final_state, state, torch.float32, device)
     _check_ckpt(checkpoint, grad_h.shape, device)
     made = []
-    out = _scan_grads(grad_h, state, want_initial_state_grad, made)
+    out = _scan_grads(grad_h, state, grad_final_state, want_initial_state_grad, made)
     ws, nbytes = _scan_workspace(workspace, grad_h, B, T, D, seqs, code, 0, made)
     _scan_call("kda_scan_backward_ckpt", device, stream,
                (checkpoint.data_ptr(), grad_h.data_ptr(), _at(grad_final_state), _at(cu_seqlens), seqs,
