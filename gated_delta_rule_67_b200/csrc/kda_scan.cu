@@ -629,19 +629,42 @@ __global__ void __launch_bounds__(kThreads, Shape<K, IO, COMPL>::kPerSm)
 
     // bit r: whether this thread's row r belongs to a sequence, is where the recurrence starts, and ends
     uint32_t valid = 0, start = 0, stop = 0;
+    // Rows as they come in most tiles (0), with at most one start and one stop in a segment (1: masked by selects,
+    // which is 5 us quicker at the ends of a chain than branches), any (2).
+    int kind = 0;
+    f2 begins = 0, ends = 0;  // kind 1: the state (gradient) where it starts; backward: the state before its last row
     if (edge) {
-#pragma unroll 1
-      for (int r = 0; r < R; ++r) {
-        const Row o = row_info(q, row_at(r));
-        valid |= (uint32_t)o.valid << r;
-        start |= (uint32_t)(o.valid && (kDown ? o.last : o.first)) << r;
-        stop |= (uint32_t)(o.valid && (kDown ? o.first : o.last)) << r;
+      if (packed) {
+#pragma unroll
+        for (int r = 0; r < R; ++r) {
+          const int v = sh.info[q.s][row_at(r)];
+          const uint32_t first = v >= 0 && (v & 2), last = v >= 0 && (v & 1);
+          valid |= (v >= 0 ? 1u : 0u) << r;
+          start |= (kDown ? last : first) << r;
+          stop |= (kDown ? first : last) << r;
+        }
+      } else {
+        const int t = q.t0 + row_at(0);
+        if (kDown) {  // rows t, t - 1, ..
+          const int skip = min(max(t - a.T + 1, 0), R), last = t - (a.T - 1);
+          valid = (1u << R) - (1u << skip);
+          start = last >= 0 && last < R ? 1u << last : 0u;
+          stop = t < R ? 1u << t : 0u;
+        } else {
+          const int last = a.T - 1 - t;
+          valid = (1u << min(max(a.T - t, 0), R)) - 1;
+          start = t == 0 ? 1u : 0u;
+          stop = last >= 0 && last < R ? 1u << last : 0u;
+        }
       }
+      kind = __any_sync(0xffffffffu, (start & (start - 1)) | (stop & (stop - 1))) || !p.tma ? 2 : 1;
+      if (kind == 1 && start) begins = state_of(q, a.s0, row_info(q, row_at(__ffs(start) - 1)).seq);
+      if (K == kBwd && kind == 1 && stop) ends = state_of(q, a.h0, row_info(q, row_at(__ffs(stop) - 1)).seq);
     }
     // ---- segments as pairs
     f2 al[R], in[R];  // alpha; forward: the input, backward: 1 - alpha
     auto reduce = [&](auto edges) {
-      constexpr bool E = decltype(edges)::value;
+      constexpr int E = decltype(edges)::value;
       f2 A = both(1.f), B = both(0.f);
 #pragma unroll
       for (int r = 0; r < R; ++r) {
@@ -649,11 +672,22 @@ __global__ void __launch_bounds__(kThreads, Shape<K, IO, COMPL>::kPerSm)
         f2 g, be = 0;
         if constexpr (kFrom) g = codes_of(q, 1, i);
         else g = load2(q, 1, i);
-        const f2 x = load2(q, 0, i);
+        f2 x = load2(q, 0, i);
         gate<RAW && !kFrom, RAW || COMPL>(g, al[r], be);
         in[r] = kDown && (RAW || COMPL) ? be : COMPL ? mul2(be, x) : x;
-        if (E && !(valid >> r & 1)) continue;
-        if (E && (start >> r & 1)) {
+        const bool in_it = valid >> r & 1, starts = start >> r & 1;
+        if (E == 1) {  // a row of no sequence changes nothing
+          al[r] = in_it ? al[r] : both(1.f);
+          if (kDown) x = in_it ? x : both(0.f);
+          else in[r] = in_it ? in[r] : both(0.f);
+          if (!kDown) in[r] = starts ? fma2(al[r], begins, in[r]) : in[r];
+          A = starts ? both(-0.f) : mul2(A, al[r]);
+          if (kDown) B = mul2(al[r], add2(starts ? begins : B, x));
+          else B = starts ? in[r] : fma2(al[r], B, in[r]);
+          continue;
+        }
+        if (E == 2 && !in_it) continue;
+        if (E == 2 && starts) {
           const f2 f = state_of(q, a.s0, row_info(q, i).seq);
           if (!kDown) in[r] = fma2(al[r], f, in[r]);
           A = both(-0.f);
@@ -668,10 +702,13 @@ __global__ void __launch_bounds__(kThreads, Shape<K, IO, COMPL>::kPerSm)
       unpack(B, f.y, f.w);
       *reinterpret_cast<float4*>(S::kSide == 1 ? &pair[warp][across * 2] : &sh.seg[warp][side][across * 2]) = f;
     };
-    if (edge)
-      reduce(std::true_type{});
+    using std::integral_constant;
+    if (kind == 0)
+      reduce(integral_constant<int, 0>{});
+    else if (kind == 1)
+      reduce(integral_constant<int, 1>{});
     else
-      reduce(std::false_type{});
+      reduce(integral_constant<int, 2>{});
     [[maybe_unused]] float2 sg[S::kSide];
     if constexpr (S::kSide > 1) {  // the unit's pair
       __syncwarp();
@@ -794,53 +831,65 @@ __global__ void __launch_bounds__(kThreads, Shape<K, IO, COMPL>::kPerSm)
       else
         put<IO>(place, w[0], w[1]);
     };
+    auto state_out = [&](f2 v, int i) {
+      float w[2];
+      unpack(v, w[0], w[1]);
+      float* to = a.sT + (size_t)row_info(q, i).seq * a.D + q.c;
+#pragma unroll
+      for (int j = 0; j < 2; ++j)
+        if (j < q.n) to[j] = w[j];
+    };
     auto emit = [&](auto edges, auto pitched) {
-      constexpr bool E = decltype(edges)::value;
-      const bool direct = E ? !p.tma : !decltype(pitched)::value;
+      constexpr int E = decltype(edges)::value;
+      const bool direct = E == 2 ? !p.tma : !decltype(pitched)::value;
+      f2 final = 0;
 #pragma unroll
       for (int r = 0; r < R; ++r) {
         const int i = row_at(r);
-        if (E && !(valid >> r & 1)) {  // past the end, or a row that no sequence owns
+        const bool in_it = E == 0 || (valid >> r & 1), starts = E > 0 && (start >> r & 1), stops = E > 0 && (stop >> r & 1);
+        if (E == 2 && !in_it) {  // past the end, or a row that no sequence owns
           if (!direct || q.t0 + i < a.T) {
             store(static_cast<IO*>(a.out), elem(q, 0, i), i, both(0.f), direct);
             if (kDown) store(static_cast<IO*>(a.dg), second(i), i, both(0.f), direct);
           }
           continue;
         }
-        const bool starts = E && (start >> r & 1);
         if constexpr (!kDown) {
           h = starts ? in[r] : fma2(al[r], h, in[r]);
-          store(static_cast<IO*>(a.out), elem(q, 0, i), i, h, direct);
+          store(static_cast<IO*>(a.out), elem(q, 0, i), i, in_it ? h : both(0.f), direct);
         } else {
-          f2 z;
+          f2 z, x = load2(q, 0, i);
           if constexpr (kFrom) z = codes_of(q, 2, i);
           else {
-            z = E && (stop >> r & 1) ? state_of(q, a.h0, row_info(q, i).seq) : load2(q, 2, i);
+            if (E == 2 && stops) z = state_of(q, a.h0, row_info(q, i).seq);
+            else z = load2(q, 2, i);
+            if (E == 1) z = stops ? ends : z;
             if (COMPL) z = add2(z, neg2(load2(q, 3, i)));
           }
-          const f2 d = add2(load2(q, 0, i), starts ? state_of(q, a.s0, row_info(q, i).seq) : h);
+          f2 from = h;
+          if (E == 1) from = starts ? begins : h, x = in_it ? x : both(0.f);
+          if (E == 2 && starts) from = state_of(q, a.s0, row_info(q, i).seq);
+          const f2 d = add2(x, from);
           h = mul2(al[r], d);
           f2 dg = mul2(h, z);
           if (RAW) dg = mul2(dg, in[r]);
-          store(static_cast<IO*>(a.out), elem(q, 0, i), i, COMPL ? mul2(in[r], d) : d, direct);
-          store(static_cast<IO*>(a.dg), second(i), i, dg, direct);
+          const f2 dx = COMPL ? mul2(in[r], d) : d;
+          store(static_cast<IO*>(a.out), elem(q, 0, i), i, in_it ? dx : both(0.f), direct);
+          store(static_cast<IO*>(a.dg), second(i), i, in_it ? dg : both(0.f), direct);
         }
-        if (E && (stop >> r & 1) && a.sT) {
-          float w[2];
-          unpack(h, w[0], w[1]);
-          float* to = a.sT + (size_t)row_info(q, i).seq * a.D + q.c;
-#pragma unroll
-          for (int j = 0; j < 2; ++j)
-            if (j < q.n) to[j] = w[j];
-        }
+        if (E == 1) final = stops ? h : final;
+        if (E == 2 && stops && a.sT) state_out(h, i);
       }
+      if (E == 1 && stop && a.sT) state_out(final, row_at(__ffs(stop) - 1));
     };
-    if (edge) {
-      emit(std::true_type{}, std::true_type{});
+    if (kind == 1) {
+      emit(integral_constant<int, 1>{}, std::true_type{});
+    } else if (kind == 2) {
+      emit(integral_constant<int, 2>{}, std::true_type{});
     } else if (p.tma) {
-      emit(std::false_type{}, std::true_type{});
+      emit(integral_constant<int, 0>{}, std::true_type{});
     } else {
-      emit(std::false_type{}, std::false_type{});
+      emit(integral_constant<int, 0>{}, std::false_type{});
     }
 
     // ---- out by TMA, each unit's rows (rows past T are not written)
