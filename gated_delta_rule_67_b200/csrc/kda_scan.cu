@@ -639,6 +639,7 @@ __global__ void __launch_bounds__(kThreads, Shape<K, IO, COMPL>::kPerSm)
       return __uint_as_float(v);
     };
     if constexpr (kFrom) {
+      __syncwarp();  // every lane is done with the scales of the tile before
       if (lane < S::kUnitRows) {
         const int off = (int)(scale_at(q.b, q.cb, q.t0) & 15) + lowest + lane;
         sh.scale_of[warp][0][lane] = pow2(sh.scale[q.s][0][off]);
