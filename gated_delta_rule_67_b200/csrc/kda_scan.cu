@@ -409,6 +409,7 @@ struct __align__(128) Shared {
   uint64_t came[2];
   float scale_of[kWarps][2][32];           // from the checkpoint: scales of a unit's rows
   uint64_t full[S::kStages];
+  int lost[2];                             // whether a wait gave up before a tile's barrier, of two tiles
   int4 tile[S::kStages];                   // first row, chunk (-1: none left), batch, channel block
   __align__(16) int info[S::kStages][S::kL];
   __align__(16) uint8_t scale[S::kStages][2][(S::kL + 47) / 16 * 16];
@@ -539,13 +540,18 @@ __global__ void __launch_bounds__(kThreads, Shape<K, IO, COMPL>::kPerSm)
   if (threadIdx.x == 0) {
     feed(), feed();
     if (walk) expect(0, rank == 0), expect(1, false);
+    sh.lost[1] = sh.lost[0] = 0;
   }
+  __syncthreads();  // every thread sees the same first tile
 
-  // the k-th tile of this block, chunk -1 past its last
-  auto tile_of = [&](int k) {
-    const bool there = wait_for(&sh.full[k % NS], (k / NS) & 1);
-    if (!there) gave_up(202);
-    return there ? sh.tile[k % NS] : make_int4(0, -1, 0, 0);
+  // A wait that gives up ends the block's work for all of its threads after the same tile, by sh.lost, since
+  // the others would wait without end at a barrier for a thread that left alone.  Until then the thread goes
+  // on with whatever is in the stage, but not by the rows' information, which leads to memory.
+  bool failed = false;  // a wait of this thread gave up
+  // whether the k-th tile is in its stage
+  auto has_tile = [&](int k) {
+    if (!failed && !wait_for(&sh.full[k % NS], (k / NS) & 1)) failed = true, gave_up(202);
+    return !failed;
   };
   // the r-th row of this thread's segment, as a row of the tile
   auto row_at = [&](int r) {
@@ -592,9 +598,8 @@ __global__ void __launch_bounds__(kThreads, Shape<K, IO, COMPL>::kPerSm)
   };
   // rows that TMA cannot take (their pitch is no multiple of 16 bytes): each thread brings its own channels of tile k
   auto bring_tile = [&](int k) {
-    const int4 tile = tile_of(k);
-    if (tile.y >= 0) {
-      const Place q = place_of(k, tile);
+    if (has_tile(k) && sh.tile[k % NS].y >= 0) {
+      const Place q = place_of(k, sh.tile[k % NS]);
       for (int r = 0; r < R; ++r) {
         const int i = row_at(r);
         const bool in = q.t0 + i < a.T && q.n > 0;
@@ -612,10 +617,12 @@ __global__ void __launch_bounds__(kThreads, Shape<K, IO, COMPL>::kPerSm)
   };
   if (!p.tma) bring_tile(0);
 
-  bool failed = false;
-  for (int k = 0;; ++k) {
-    const int4 tile = tile_of(k);
-    if (tile.y < 0) break;
+  int k = 0;
+  for (;; ++k) {
+    has_tile(k);
+    // both written before the last barrier, so all threads read the same: chunk -1 past the last tile
+    const int4 tile = sh.tile[k % NS];
+    if (tile.y < 0 || sh.lost[(k + 1) & 1]) break;
     if (!p.tma) {
       bring_tile(k + 1);
       asm volatile("cp.async.wait_group 1;" ::: "memory");
@@ -678,6 +685,7 @@ __global__ void __launch_bounds__(kThreads, Shape<K, IO, COMPL>::kPerSm)
           stop = last >= 0 && last < R ? 1u << last : 0u;
         }
       }
+      if (failed) valid = start = stop = 0;
       kind = __any_sync(0xffffffffu, (start & (start - 1)) | (stop & (stop - 1))) || !p.tma ? 2 : 1;
       if (kind == 1 && start) begins = state_of(q, a.s0, row_info(q, row_at(__ffs(start) - 1)).seq);
       if (K == kBwd && kind == 1 && stop) ends = state_of(q, a.h0, row_info(q, row_at(__ffs(stop) - 1)).seq);
@@ -741,9 +749,10 @@ __global__ void __launch_bounds__(kThreads, Shape<K, IO, COMPL>::kPerSm)
       pair[warp][ch] = t;
     }
     if (lane == 0) bulk_wait_read();  // the tile before has left its stage
+    if (failed) sh.lost[k & 1] = 1;
     __syncthreads();  // the pairs are there, and every warp is done with the tile before
     if (threadIdx.x == 0) {
-      if (walk && k > 0) expect(k + 1, false);
+      if (walk && k > 0 && !failed) expect(k + 1, false);
       feed();  // into its stage
     }
 
@@ -924,6 +933,11 @@ __global__ void __launch_bounds__(kThreads, Shape<K, IO, COMPL>::kPerSm)
         bulk_commit();
       }
     }
+  }
+  if (sh.lost[(k + 1) & 1]) {
+    asm volatile("cp.async.wait_all;" ::: "memory");
+    if (threadIdx.x == 0)  // its copies in flight
+      for (int j = k - 1; j < k + 2; ++j) wait_for(&sh.full[j % NS], (j / NS) & 1);
   }
   if (lane == 0) bulk_wait_read();
   __syncwarp();
