@@ -354,7 +354,8 @@ def kda_backward(q, k, v, g, beta, grad_o, scale=None, initial_state=None, grad_
 
 
 def kda_scan_workspace_size(B, T, D, num_seqs=0, dtype=torch.bfloat16, checkpoint=True) -> int:
-    """Bytes of workspace the scan calls need; less where kda_scan_fwd writes no checkpoint."""
+    """Bytes of workspace the scan calls need; less where kda_scan_fwd writes no checkpoint.  A call clears the
+    workspace's header; kda_chunk_fwd_check(workspace) tells afterwards whether a wait in the kernel gave up."""
     return int(load().kda_scan_workspace_size_ex(B, T, D, num_seqs, _dtype_code(dtype), int(checkpoint)))
 
 
@@ -402,18 +403,18 @@ def _state_like(given, shape, device):
     return torch.empty(shape, dtype=torch.float32, device=device) if given is None else torch.empty_like(given)
 
 
-def _scan_call(name, device, stream, args, made):
+def _scan_call(name, device, stream, args, made, need=None, workspace=None):
     """One call of the library on the device's stream.  ``made``: the tensors allocated here, which a stream
-    other than the current one must be recorded with."""
+    other than the current one must be recorded with.  ``need``: for calls with a workspace, its size."""
     fn = getattr(_lib or load(), name)
     index = device.index
     current = torch._C._cuda_getCurrentRawStream(index)
     raw = current if stream is None else stream.cuda_stream
     if torch.cuda.current_device() == index:
-        st = fn(*args, raw)
+        st = _scan_launch(fn, args, need, workspace, raw)
     else:
         with _on(device):
-            st = fn(*args, raw)
+            st = _scan_launch(fn, args, need, workspace, raw)
     if raw != current:
         for t in made:
             t.record_stream(stream)
@@ -421,19 +422,26 @@ def _scan_call(name, device, stream, args, made):
         raise KDAError(st, name)
 
 
-def _scan_workspace(workspace, x, B, T, D, seqs, code, checkpoint, made):
-    """(address, bytes) of the caller's workspace or of one made here."""
-    if workspace is None:
-        need = _scan_need(B, T, D, seqs, code, checkpoint)
-        if not need:
-            return None, 0
-        workspace = torch.empty(need, dtype=torch.uint8, device=x.device)
-        made.append(workspace)
-    else:
-        _check_dev("workspace", workspace)
-        if workspace.device != x.device:
-            raise ValueError(f"workspace must live on {x.device}")
-    return workspace.data_ptr(), workspace.numel() * workspace.element_size()
+def _scan_launch(fn, args, need, workspace, raw):
+    if need is None:
+        return fn(*args, raw)
+    if workspace is not None:
+        return fn(*args, workspace.data_ptr(), workspace.numel() * workspace.element_size(), raw)
+    if not need:
+        return fn(*args, None, 0, raw)
+    # Memory of the stream that the kernels run on, given back at once: whoever gets it next comes after them there.
+    # A tensor for it would take 1.5 us of a short call's 14, this 0.6.
+    at = torch._C._cuda_cudaCachingAllocator_raw_alloc(need, raw)
+    try:
+        return fn(*args, at, need, raw)
+    finally:
+        torch._C._cuda_cudaCachingAllocator_raw_delete(at)
+
+
+def _check_scan_workspace(workspace, device):
+    _check_dev("workspace", workspace)
+    if workspace.device != device:
+        raise ValueError(f"workspace must live on {device}")
 
 
 def kda_scan_fwd(x, g, initial_state=None, *, cu_seqlens=None, input_gate=KDA_SCAN_INPUT_PLAIN, prep=0, h=None,
@@ -469,10 +477,12 @@ def kda_scan_fwd(x, g, initial_state=None, *, cu_seqlens=None, input_gate=KDA_SC
         made.append(final_state)
     if checkpoint is not None:
         _check_ckpt(checkpoint, x.shape, device)
-    ws, nbytes = _scan_workspace(workspace, x, B, T, D, seqs, code, checkpoint is not None, made)
+    if workspace is not None:
+        _check_scan_workspace(workspace, device)
     _scan_call("kda_scan_fwd", device, stream,
                (x.data_ptr(), g.data_ptr(), _at(initial_state), _at(cu_seqlens), seqs, h.data_ptr(), _at(final_state),
-                _at(checkpoint), B, T, D, code, prep, input_gate, ws, nbytes), made)
+                _at(checkpoint), B, T, D, code, prep, input_gate), made,
+               _scan_need(B, T, D, seqs, code, checkpoint is not None), workspace)
     return h, final_state
 
 
@@ -515,11 +525,12 @@ def kda_scan_backward(x, g, h, grad_h, initial_state=None, grad_final_state=None
     made = []
     out = _scan_grads(grad_h, state, grad_final_state if grad_final_state is not None else initial_state,
                       want_initial_state_grad, made)
-    ws, nbytes = _scan_workspace(workspace, grad_h, B, T, D, seqs, code, 0, made)
+    if workspace is not None:
+        _check_scan_workspace(workspace, device)
     _scan_call("kda_scan_backward", device, stream,
                (_at(x), g.data_ptr(), h.data_ptr(), _at(initial_state), grad_h.data_ptr(), _at(grad_final_state),
                 _at(cu_seqlens), seqs, out["dx"].data_ptr(), out["dg"].data_ptr(), _at(out["dS0"]), B, T, D, code, prep,
-                input_gate, ws, nbytes), made)
+                input_gate), made, _scan_need(B, T, D, seqs, code, False), workspace)
     return out
 
 
@@ -537,11 +548,12 @@ def kda_scan_backward_ckpt(checkpoint, grad_h, grad_final_state=None, *, cu_seql
     _check_ckpt(checkpoint, grad_h.shape, device)
     made = []
     out = _scan_grads(grad_h, state, grad_final_state, want_initial_state_grad, made)
-    ws, nbytes = _scan_workspace(workspace, grad_h, B, T, D, seqs, code, 0, made)
+    if workspace is not None:
+        _check_scan_workspace(workspace, device)
     _scan_call("kda_scan_backward_ckpt", device, stream,
                (checkpoint.data_ptr(), grad_h.data_ptr(), _at(grad_final_state), _at(cu_seqlens), seqs,
-                out["dx"].data_ptr(), out["dg"].data_ptr(), _at(out["dS0"]), B, T, D, code, prep, input_gate, ws,
-                nbytes), made)
+                out["dx"].data_ptr(), out["dg"].data_ptr(), _at(out["dS0"]), B, T, D, code, prep, input_gate), made,
+               _scan_need(B, T, D, seqs, code, False), workspace)
     return out
 
 

@@ -379,11 +379,6 @@ static kda_status scan_checks(const kda::ScanArgs& a, const Range* in, int n_in,
   return KDA_OK;
 }
 
-// The workspace of a call that needs one, else null (nothing is written to a buffer it does not need).
-static void* scan_workspace(const kda::ScanArgs& a, void* workspace) {
-  return kda::scan_workspace_bytes(a.B, a.T, a.D, a.N, a.dtype, a.ckpt && !a.dy) ? workspace : nullptr;
-}
-
 static kda_status scan_flags(int64_t B, int64_t T, int64_t D, const int32_t* cu, int64_t num_seqs, int dtype, int prep,
                              int input_gate) {
   const kda_status st = scan_sizes(B, T, D, cu ? num_seqs : 0, dtype);
@@ -421,7 +416,7 @@ kda_status kda_scan_fwd(const void* x, const void* g, const float* initial_state
   st = scan_checks(a, in, 4, out, 3, need, 3, workspace, workspace_bytes);
   if (st != KDA_OK) return st;
   if (B == 0 || T == 0) return scan_empty(initial_state, final_state, sb, stream);
-  return from_cuda(kda::launch_scan_fwd(a, scan_workspace(a, workspace), stream));
+  return from_cuda(kda::launch_scan_fwd(a, workspace, stream));
 }
 
 kda_status kda_scan_backward(const void* x, const void* g, const void* h, const float* initial_state,
@@ -448,7 +443,7 @@ kda_status kda_scan_backward(const void* x, const void* g, const void* h, const 
   st = scan_checks(a, in, 7, out, 3, need, 6, workspace, workspace_bytes);
   if (st != KDA_OK) return st;
   if (B == 0 || T == 0) return scan_empty(grad_final_state, grad_initial_state, sb, stream);
-  return from_cuda(kda::launch_scan_bwd(a, scan_workspace(a, workspace), stream));
+  return from_cuda(kda::launch_scan_bwd(a, workspace, stream));
 }
 
 kda_status kda_scan_backward_ckpt(const void* checkpoint, const void* grad_h, const float* grad_final_state,
@@ -472,7 +467,7 @@ kda_status kda_scan_backward_ckpt(const void* checkpoint, const void* grad_h, co
   st = scan_checks(a, in, 4, out, 3, need, 4, workspace, workspace_bytes);
   if (st != KDA_OK) return st;
   if (B == 0 || T == 0) return scan_empty(grad_final_state, grad_initial_state, sb, stream);
-  return from_cuda(kda::launch_scan_bwd(a, scan_workspace(a, workspace), stream));
+  return from_cuda(kda::launch_scan_bwd(a, workspace, stream));
 }
 
 kda_status kda_scan_step(const void* x, const void* g, const float* state, float* out_state, void* h, int N, int D,

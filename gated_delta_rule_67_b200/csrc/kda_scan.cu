@@ -451,10 +451,9 @@ __global__ void __launch_bounds__(kThreads, Shape<K, IO, COMPL>::kPerSm)
     __syncthreads();
   }
   grid_dep_wait();  // the workspace was prepared, and the inputs written, by earlier kernels
-  if (walk && p.hdr && blockIdx.x == 0 && threadIdx.x == 0) p.hdr->error = 0;
+  if (walk && blockIdx.x == 0 && threadIdx.x == 0) p.hdr->error = 0;  // long before the first wait can give up
 
   auto gave_up = [&](uint32_t where) {
-    if (!p.hdr) return;
     atomicOr(&p.hdr->error, 1u);
     atomicExch(&p.hdr->where, where);
   };
@@ -1292,7 +1291,7 @@ cudaError_t launch_tiles(const ScanArgs& a, void* ws, cudaStream_t stream) {
   p.tma = (size_t)a.D * sizeof(IO) % 16 == 0;
   p.words = (size_t)a.D * sizeof(IO) % 4 == 0;
   uint8_t* w = static_cast<uint8_t*>(ws);
-  p.hdr = ws ? reinterpret_cast<WorkspaceHeader*>(w) : nullptr;
+  p.hdr = reinterpret_cast<WorkspaceHeader*>(w);
   w += sizeof(WorkspaceHeader);
   p.pairs = reinterpret_cast<float*>(w);
   p.states = p.pairs + plan.pair_words;
@@ -1347,9 +1346,10 @@ cudaError_t launch_tiles(const ScanArgs& a, void* ws, cudaStream_t stream) {
 
 }  // namespace
 
-// Enough for every kind of call of these sizes: the header, the words handed
-// between blocks, the rows' information if packed, the forward's states at its
-// segments for the checkpoint.
+// Enough for every kind of call of these sizes: the header, whose error word
+// tells of a wait that gave up, the words handed between blocks, the rows'
+// information if packed, the forward's states at its segments for the
+// checkpoint.
 size_t scan_workspace_bytes(int B, int T, int D, int N, int dtype, bool checkpoint) {
   if (B == 0 || T == 0) return 0;
   size_t words = 0, enters = 0;
@@ -1366,8 +1366,8 @@ size_t scan_workspace_bytes(int B, int T, int D, int N, int dtype, bool checkpoi
     fit_all(float{});
   else
     fit_all(__nv_bfloat16{});
-  const size_t bytes = align256(words * 4) + (N > 0 ? info_bytes(T) : 0) + (checkpoint ? align256(enters * 4) : 0);
-  return bytes ? sizeof(WorkspaceHeader) + bytes : 0;
+  return sizeof(WorkspaceHeader) + align256(words * 4) + (N > 0 ? info_bytes(T) : 0) +
+         (checkpoint ? align256(enters * 4) : 0);
 }
 
 cudaError_t launch_scan_fwd(const ScanArgs& a, void* ws, cudaStream_t stream) {

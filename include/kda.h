@@ -372,8 +372,9 @@ typedef enum { KDA_SCAN_INPUT_PLAIN = 0, KDA_SCAN_INPUT_COMPLEMENT = 1 } kda_sca
 
 /*
  * Bytes of device workspace that kda_scan_fwd without a checkpoint,
- * kda_scan_backward and kda_scan_backward_ckpt need; 0 if none (for many sizes;
- * NULL is then allowed), and for arguments they reject.
+ * kda_scan_backward and kda_scan_backward_ckpt need: for many sizes no more than
+ * the header (256); 0 for B = 0 or T = 0 (NULL is then allowed), and for
+ * arguments they reject.
  * `num_seqs`: the number of packed sequences, 0 without cu_seqlens.
  */
 KDA_API size_t kda_scan_workspace_size(int B, int T, int D, int num_seqs, int dtype);
@@ -414,9 +415,10 @@ KDA_API size_t kda_scan_checkpoint_size(int B, int T, int D);
  *                   aligned, written beside h
  *   workspace     : kda_scan_workspace_size_ex() bytes, 256-byte aligned,
  *                   contents on entry do not matter; not shared by two calls
- *                   in flight (two captured graphs among them).  Its header is
- *                   read by kda_chunk_fwd_check: KDA_ERR_TIMEOUT if a bounded
- *                   wait inside the kernel gave up (outputs not valid).
+ *                   in flight (two captured graphs among them).  Every call
+ *                   clears its header; kda_chunk_fwd_check reads it afterwards:
+ *                   KDA_ERR_TIMEOUT if a bounded wait inside the kernel gave up
+ *                   (outputs not valid).
  * Results do not depend on the order in which the GPU runs the blocks.
  * B = 0 or T = 0 is valid: the final state is the initial state.
  */
