@@ -403,21 +403,32 @@ def _state_like(given, shape, device):
     return torch.empty(shape, dtype=torch.float32, device=device) if given is None else torch.empty_like(given)
 
 
-def _scan_call(name, device, stream, args, made, need=None, workspace=None):
-    """One call of the library on the device's stream.  ``made``: the tensors allocated here, which a stream
-    other than the current one must be recorded with.  ``need``: for calls with a workspace, its size."""
+def _scan_on(stream, device, call, *args, **kw):
+    """A scan call on ``stream``.  What it allocates is memory of that stream: memory of the current one may still
+    be in use by work that the kernel would not wait for.  The results are recorded with the current stream, where
+    the caller goes on with them."""
+    if stream.device != device:
+        raise ValueError(f"stream must belong to {device}, not {stream.device}")
+    current = torch.cuda.current_stream(device)
+    if stream == current:
+        return call(*args, **kw)
+    with torch.cuda.stream(stream):
+        out = call(*args, **kw)
+    for t in out.values() if isinstance(out, dict) else out if isinstance(out, tuple) else (out,):
+        if t is not None:
+            t.record_stream(current)
+    return out
+
+
+def _scan_call(name, device, args, need=None, workspace=None):
+    """One call of the library on the device's current stream.  ``need``: for calls with a workspace, its size."""
     fn = getattr(_lib or load(), name)
-    index = device.index
-    current = torch._C._cuda_getCurrentRawStream(index)
-    raw = current if stream is None else stream.cuda_stream
-    if torch.cuda.current_device() == index:
+    raw = torch._C._cuda_getCurrentRawStream(device.index)
+    if torch.cuda.current_device() == device.index:
         st = _scan_launch(fn, args, need, workspace, raw)
     else:
         with _on(device):
             st = _scan_launch(fn, args, need, workspace, raw)
-    if raw != current:
-        for t in made:
-            t.record_stream(stream)
     if st != KDA_OK:
         raise KDAError(st, name)
 
@@ -458,30 +469,31 @@ def kda_scan_fwd(x, g, initial_state=None, *, cu_seqlens=None, input_gate=KDA_SC
     ``initial_state`` itself.
     """
     _check_dev("x", x)
+    if stream is not None:
+        return _scan_on(stream, x.device, kda_scan_fwd, x, g, initial_state, cu_seqlens=cu_seqlens, input_gate=input_gate,
+                        prep=prep, h=h, final_state=final_state, output_final_state=output_final_state,
+                        checkpoint=checkpoint, workspace=workspace)
     device, dtype, code = x.device, x.dtype, _dtype_code(x.dtype)
     B, T, D, seqs = _scan_sizes(x, cu_seqlens)
     state = (seqs or B, D)
     _same("g", g, x.shape, dtype, device)
     if initial_state is not None:
         _same("initial_state", initial_state, state, torch.float32, device)
-    made = []
     if h is None:
         h = torch.empty_like(x)
-        made.append(h)
     else:
         _same("h", h, x.shape, dtype, device)
     if final_state is not None:
         _same("final_state", final_state, state, torch.float32, device)
     elif output_final_state:
         final_state = _state_like(initial_state, state, device)
-        made.append(final_state)
     if checkpoint is not None:
         _check_ckpt(checkpoint, x.shape, device)
     if workspace is not None:
         _check_scan_workspace(workspace, device)
-    _scan_call("kda_scan_fwd", device, stream,
+    _scan_call("kda_scan_fwd", device,
                (x.data_ptr(), g.data_ptr(), _at(initial_state), _at(cu_seqlens), seqs, h.data_ptr(), _at(final_state),
-                _at(checkpoint), B, T, D, code, prep, input_gate), made,
+                _at(checkpoint), B, T, D, code, prep, input_gate),
                _scan_need(B, T, D, seqs, code, checkpoint is not None), workspace)
     return h, final_state
 
@@ -493,11 +505,10 @@ def _check_ckpt(checkpoint, shape, device):
         raise ValueError(f"checkpoint must hold {need} bytes on {device}")
 
 
-def _scan_grads(like, state, given, want_initial_state_grad, made):
+def _scan_grads(like, state, given, want_initial_state_grad):
     out = dict(dx=torch.empty_like(like), dg=torch.empty_like(like), dS0=None)
     if want_initial_state_grad:
         out["dS0"] = _state_like(given, state, like.device)
-    made.extend(t for t in out.values() if t is not None)
     return out
 
 
@@ -509,6 +520,10 @@ def kda_scan_backward(x, g, h, grad_h, initial_state=None, grad_final_state=None
     KDA_SCAN_INPUT_PLAIN.  Returns a dict: dx, dg (input dtype) and dS0 fp32 (None if not wanted).
     """
     _check_dev("grad_h", grad_h)
+    if stream is not None:
+        return _scan_on(stream, grad_h.device, kda_scan_backward, x, g, h, grad_h, initial_state, grad_final_state,
+                        cu_seqlens=cu_seqlens, input_gate=input_gate, prep=prep, workspace=workspace,
+                        want_initial_state_grad=want_initial_state_grad)
     device, dtype, code = grad_h.device, grad_h.dtype, _dtype_code(grad_h.dtype)
     B, T, D, seqs = _scan_sizes(grad_h, cu_seqlens)
     state = (seqs or B, D)
@@ -522,15 +537,14 @@ def kda_scan_backward(x, g, h, grad_h, initial_state=None, grad_final_state=None
         _same("initial_state", initial_state, state, torch.float32, device)
     if grad_final_state is not None:
         _same("grad_final_state", grad_final_state, state, torch.float32, device)
-    made = []
     out = _scan_grads(grad_h, state, grad_final_state if grad_final_state is not None else initial_state,
-                      want_initial_state_grad, made)
+                      want_initial_state_grad)
     if workspace is not None:
         _check_scan_workspace(workspace, device)
-    _scan_call("kda_scan_backward", device, stream,
+    _scan_call("kda_scan_backward", device,
                (_at(x), g.data_ptr(), h.data_ptr(), _at(initial_state), grad_h.data_ptr(), _at(grad_final_state),
                 _at(cu_seqlens), seqs, out["dx"].data_ptr(), out["dg"].data_ptr(), _at(out["dS0"]), B, T, D, code, prep,
-                input_gate), made, _scan_need(B, T, D, seqs, code, False), workspace)
+                input_gate), _scan_need(B, T, D, seqs, code, False), workspace)
     return out
 
 
@@ -540,19 +554,22 @@ def kda_scan_backward_ckpt(checkpoint, grad_h, grad_final_state=None, *, cu_seql
     """kda_scan_backward from the 8-bit checkpoint that kda_scan_fwd filled (same sizes, ``prep``, ``input_gate``
     and ``cu_seqlens``) in place of x, g, h and the initial state."""
     _check_dev("grad_h", grad_h)
+    if stream is not None:
+        return _scan_on(stream, grad_h.device, kda_scan_backward_ckpt, checkpoint, grad_h, grad_final_state,
+                        cu_seqlens=cu_seqlens, input_gate=input_gate, prep=prep, workspace=workspace,
+                        want_initial_state_grad=want_initial_state_grad)
     device, code = grad_h.device, _dtype_code(grad_h.dtype)
     B, T, D, seqs = _scan_sizes(grad_h, cu_seqlens)
     state = (seqs or B, D)
     if grad_final_state is not None:
         _same("grad_final_state", grad_final_state, state, torch.float32, device)
     _check_ckpt(checkpoint, grad_h.shape, device)
-    made = []
-    out = _scan_grads(grad_h, state, grad_final_state, want_initial_state_grad, made)
+    out = _scan_grads(grad_h, state, grad_final_state, want_initial_state_grad)
     if workspace is not None:
         _check_scan_workspace(workspace, device)
-    _scan_call("kda_scan_backward_ckpt", device, stream,
+    _scan_call("kda_scan_backward_ckpt", device,
                (checkpoint.data_ptr(), grad_h.data_ptr(), _at(grad_final_state), _at(cu_seqlens), seqs,
-                out["dx"].data_ptr(), out["dg"].data_ptr(), _at(out["dS0"]), B, T, D, code, prep, input_gate), made,
+                out["dx"].data_ptr(), out["dg"].data_ptr(), _at(out["dS0"]), B, T, D, code, prep, input_gate),
                _scan_need(B, T, D, seqs, code, False), workspace)
     return out
 
@@ -561,13 +578,14 @@ def kda_scan_step(x, g, state, *, input_gate=KDA_SCAN_INPUT_PLAIN, prep=0, h=Non
     """One token of the elementwise recurrence for N sequences: x, g [N,D], state [N,D] fp32, updated in place, or
     left and the new one written to ``out_state``.  Returns h [N,D] in the input dtype."""
     _check_dev("x", x)
+    if stream is not None:
+        return _scan_on(stream, x.device, kda_scan_step, x, g, state, input_gate=input_gate, prep=prep, h=h,
+                        out_state=out_state)
     device, code = x.device, _dtype_code(x.dtype)
     if x.dim() != 2:
         raise ValueError("x must be [N,D]")
-    made = []
     if h is None:
         h = torch.empty_like(x)
-        made.append(h)
     else:
         _same("h", h, x.shape, x.dtype, device)
     _same("g", g, x.shape, x.dtype, device)
@@ -576,7 +594,7 @@ def kda_scan_step(x, g, state, *, input_gate=KDA_SCAN_INPUT_PLAIN, prep=0, h=Non
         out_state = state
     else:
         _same("out_state", out_state, x.shape, torch.float32, device)
-    _scan_call("kda_scan_step", device, stream,
+    _scan_call("kda_scan_step", device,
                (x.data_ptr(), g.data_ptr(), state.data_ptr(), out_state.data_ptr(), h.data_ptr(), x.shape[0], x.shape[1],
-                code, prep, input_gate), made)
+                code, prep, input_gate))
     return h
