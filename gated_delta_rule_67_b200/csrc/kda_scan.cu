@@ -61,8 +61,11 @@ constexpr int kWarps = 8;
 constexpr int kThreads = 32 * kWarps;
 constexpr int kGroup = 16;      // few chains: tiles from one published state to the next
 constexpr int kCluster = 8;     // blocks that walk a chain together, at most
-// Fewer chains than this, of more tiles than this each, are joined tile by tile instead of walked (bf16 forward,
-// 65536 rows: 2 chains 44 us against 88, 8 chains 73 against 90; 15 chains 100 against 91, 32 chains 171 against 107).
+// Fewer chains than this, of more tiles than this each, are joined tile by tile instead of walked.  Measured, walked /
+// joined, us: over 256 tiles the bf16 forward with 2 chains 73 / 24, 8 73 / 50, 12 74 / 67, 16 96 / 89, 24 99 / 117; the
+// fp32 forward 57 / 22, 59 / 43, 59 / 59, 70 / 77, 72 / 103; the backward and the one from the checkpoint cross between
+// 12 and 24 chains too, but for the fp32 backward (4 chains 67 / 42, 8 67 / 76).  4 chains of 16 tiles 14 / 16, of 32
+// 17 / 16 (fp32 14 / 16), of 64 24 / 17.
 constexpr int kJoinChains = 12, kJoinTiles = 32;
 // Chains of 64 channels from which on the backward from the checkpoint takes them (see Shape).
 constexpr int kWideChains = 128;
@@ -349,15 +352,18 @@ enum Kind { kFwd, kBwd, kBwdCkpt, kBwdCkptNarrow };
 // that the segments side by side in a warp lie in different banks, and as
 // large as registers and the stages of two blocks in an SM's shared memory
 // allow.  Rows are 64 bytes of bf16 or fp32.  From the checkpoint, whose codes
-// are one byte, 64 channels are best for bf16 where the chains are many (143
-// us against 163 with 32 at B8 T4096 D2048), 32 where they are few (32767 packed
-// rows of 1024 channels, forward and backward: 324 us against 396 at the time);
-// fp32 takes 32.
+// are one byte, bf16 takes 64 channels where the chains of 64 are many and 32
+// where they are few: over 8192 rows, 64 / 32 channels, us, raw gates with 1 -
+// alpha and log-gates with 1: 32 chains 49 / 49 and 43 / 43, 64 83 / 84 and 69 /
+// 74, 96 147 / 153 and 124 / 135, 128 the same, 192 (where the last wave of 32 is
+// fuller) 280 / 248 and 232 / 225, 256 280 / 298 and 232 / 262.  fp32 takes 32.
 //
-// Measured, bf16: forward B1 T65536 D4096 282-319 us (5.0-5.7 TB/s), backward
-// 495-552 us; B8 T4096 D2048 with raw gates 107 us, backward 164-174 us, from the
-// checkpoint 140 us.  Bound by issue (20 to 39 instructions an element, 110 to
-// 128 registers, two blocks of 8 warps per SM) more than by memory.
+// Measured, bf16: forward B1 T65536 D4096 321-345 us (4.7-5.0 TB/s), backward
+// 542-590 us; B8 T4096 D2048 with raw gates 103 us, backward 168-174 us, from the
+// checkpoint 144-147 us.  Two blocks of 8 warps per SM (110 to 128 registers)
+// issue on 46 to 54 % of the cycles: 24 to 42 instructions an element, most of
+// the waiting for results of fixed latency (1.3 to 1.8 warps per issue), for
+// barriers (0.7 to 0.8) and shared memory (0.6 to 0.7), more than for DRAM.
 template <Kind K, typename IO, bool COMPL>
 struct Shape {
   static constexpr bool kDown = K != kFwd;
@@ -963,9 +969,11 @@ __device__ __forceinline__ f2 log1p2_of(f2 e) {
 // The 8-bit checkpoint.  A block writes 128 channels (a row's scale block) of
 // four segments of the forward's rows; a thread holds two channels x one
 // segment, as there, and goes the same way from the state that entered the
-// segment, so that z is what the forward saw.  8 B of traffic per element in
-// bf16 (x and g are read once more, from L2 for the rows that the forward did
-// last, which come first here); all loads of a thread are in flight at once.
+// segment, so that z is what the forward saw.  In bf16 it touches 6.3 B per
+// element: x and g once more (from L2 for the rows that the forward did last,
+// which come first here), the two codes, the states; 5.5 of them in DRAM (33.5 M
+// elements, 96 us).  58 instructions an element, issued on 60 % of the cycles.
+// All loads of a thread are in flight at once.
 template <typename IO, bool RAW, bool COMPL>
 __global__ void __launch_bounds__(256, 2) scan_save_kernel(const __grid_constant__ TileArgs p) {
   using S = Shape<kFwd, IO, COMPL>;

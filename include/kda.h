@@ -356,7 +356,9 @@ KDA_API kda_status kda_recurrent_step_ex(const void* q, const void* k, const voi
  *
  * Layout: x, g, h and their gradients are [B, T, D] (dtype, contiguous, any
  * D >= 1); initial_state and final_state are [B, D] fp32.  State, sums and
- * products are fp32; h and the gradients are rounded once.
+ * products are fp32; h and the gradients are rounded once.  Rows are taken
+ * together in stretches: where the product of a stretch's alpha underflows to
+ * 0, an infinite state that enters it comes out as NaN, not as infinity.
  *
  * Packed sequences: with `cu_seqlens` non-NULL (device, int32,
  * [num_seqs + 1]), B must be 1, sequence i owns the rows
@@ -403,6 +405,16 @@ KDA_API size_t kda_scan_workspace_size_ex(int B, int T, int D, int num_seqs, int
  * bytes: lambda codes [R][P], z codes [R][P], lambda scales [K][R], z scales
  * [K][R] (bytes, k + 127).  Channels D .. P - 1 of the codes are undefined.
  * Rows outside every packed sequence hold zeros.
+ *
+ * What that costs: both numbers have 4 significant bits, lambda too, so the
+ * backward runs through slightly other gates.  With memories of a few to a
+ * thousand rows (1500 rows, 2-norm against the gradients of the activations as
+ * they were) grad_x is 0.3 % off for PLAIN and 2.3 % for COMPLEMENT, whose
+ * weight 1 - alpha comes from lambda, grad_g 2.7 % (raw gates 3.5 %),
+ * grad_initial_state 0.3 %.  A scale is shared by 128 channels, and values
+ * below 2^-10 of it become 0: beside a channel that forgets everything (lambda
+ * = -128, scale 1/2) one whose lambda is above -4.9e-4 does not forget at all in
+ * that row (2 % of the channels with such memories).
  */
 KDA_API size_t kda_scan_checkpoint_size(int B, int T, int D);
 
