@@ -427,7 +427,7 @@ KDA_API size_t kda_scan_checkpoint_size(int B, int T, int D);
  *                   aligned, written beside h
  *   workspace     : kda_scan_workspace_size_ex() bytes, 256-byte aligned,
  *                   contents on entry do not matter; not shared by two calls
- *                   in flight (two captured graphs among them).  Every call
+ *                   in flight (two captured graphs among them).  A call with rows
  *                   clears its header; kda_chunk_fwd_check reads it afterwards:
  *                   KDA_ERR_TIMEOUT if a bounded wait inside the kernel gave up
  *                   (outputs not valid).
