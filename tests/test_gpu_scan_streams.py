@@ -1,4 +1,5 @@
 """The ``stream`` argument of the scan calls: the memory that a call takes is its own, on both streams."""
+import threading
 import types
 
 import pytest
@@ -102,3 +103,32 @@ def test_a_stream_of_another_device_is_refused():
     other = types.SimpleNamespace(device=torch.device("cuda", x.device.index + 1))
     with pytest.raises(ValueError, match="stream"):
         kda_scan_fwd(x, g, stream=other)
+
+
+def test_two_threads_on_two_streams():
+    """Calls of two threads at once, each on its own stream with memory that the calls take for themselves."""
+    dev = cuda_or_skip()
+    sizes = [(1, 9000, 40), (2, 700, 264)]  # joined, walked
+    data = [inputs(dev, 20 + i, *s) for i, s in enumerate(sizes)]
+
+    def step(x, g, dh, s0):
+        h, s = kda_scan_fwd(x, g, s0)
+        return [h, s] + outputs(kda_scan_backward(None, g, h, dh, s0))
+
+    want = [step(*d) for d in data]
+    torch.cuda.synchronize()
+    wrong = []
+
+    def work(i):
+        with torch.cuda.stream(torch.cuda.Stream(dev)):
+            for _ in range(50):
+                for a, b in zip(step(*data[i]), want[i]):
+                    if not torch.equal(a, b):
+                        wrong.append(i)
+
+    threads = [threading.Thread(target=work, args=(i,)) for i in range(2)]
+    for t in threads:
+        t.start()
+    for t in threads:
+        t.join()
+    assert not wrong
